@@ -143,6 +143,39 @@ int resolve_splits(int b, int hkv, int max_seqlen_k, int num_splits, int sms) {
   return max(1, min(min(s, 64), max_useful));
 }
 
+// Page strides in elements; 0 means contiguous pages.  A given stride must
+// hold a whole page and keep 16-byte alignment (TMA).
+bool page_stride_ok(int64_t ps, int64_t page_elems) {
+  return ps == 0 || (ps >= page_elems && ps % 8 == 0 && ps <= (int64_t)1 << 40);
+}
+
+// The cache of attn_fwd_paged and attn_kvcache_append: its sizes and table.
+attn_status check_cache(const int32_t *block_table, int num_pages, int page_size,
+                        int max_pages_per_seq, int batch, int hkv, int d, int64_t k_ps,
+                        int64_t v_ps) {
+  if (num_pages < 0 || page_size <= 0 || max_pages_per_seq <= 0) return ATTN_ERR_INVALID;
+  if (!block_table && (num_pages != batch || max_pages_per_seq != 1)) return ATTN_ERR_INVALID;
+  const int64_t page_elems = (int64_t)page_size * hkv * d;
+  if (!page_stride_ok(k_ps, page_elems) || !page_stride_ok(v_ps, page_elems))
+    return ATTN_ERR_INVALID;
+  if ((int64_t)max_pages_per_seq * page_size > INT32_MAX / 2) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+// The norm and rotation arguments shared by their three entry points.
+attn_status check_rope(int dtype, int hq, int hkv, int d, const void *q_weight,
+                       const void *k_weight, float eps, const uint64_t *phases, int rot) {
+  if (dtype != ATTN_F16 && dtype != ATTN_BF16) return ATTN_ERR_INVALID;
+  if (hq < 0 || hkv < 0) return ATTN_ERR_INVALID;
+  if (d != 64 && d != 128 && d != 256) return ATTN_ERR_UNSUPPORTED;
+  if (!isfinite(eps) || eps < 0.f) return ATTN_ERR_INVALID;
+  if (rot < 0 || rot > d || rot % 16 != 0) return ATTN_ERR_INVALID;
+  if (rot > 0 && !phases) return ATTN_ERR_INVALID;
+  if (!aligned16(phases) || !aligned16(q_weight) || !aligned16(k_weight)) return ATTN_ERR_INVALID;
+  if ((int64_t)(hq > hkv ? hq : hkv) * d > INT32_MAX / 2) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
 std::atomic<unsigned long long> g_launches{0};
 
 }  // namespace
@@ -479,6 +512,271 @@ attn_status attn_fwd_fp8(const void *q, const void *k, const void *v, void *out,
   a.qk_fp8 = 1;
   a.out_scale = descale_v;
   return launched(launch_fwd_tc(a, stream));
+}
+
+size_t attn_fwd_paged_workspace_size(int batch, int total_q, int hq, int hkv, int d,
+                                     int num_splits) {
+  (void)batch; (void)total_q; (void)hq; (void)hkv; (void)d; (void)num_splits;
+  return 0;
+}
+
+attn_status attn_fwd_paged(const void *q, const void *k_cache, const void *v_cache, void *out,
+                           float *lse, int64_t q_row_stride, int64_t k_page_stride,
+                           int64_t v_page_stride, const int32_t *cu_seqlens_q,
+                           const int32_t *cache_seqlens, const int32_t *block_table,
+                           int num_pages, int page_size, int max_pages_per_seq, int appended,
+                           int batch, int total_q, int dtype, int hq, int hkv, int d, float scale,
+                           int causal, int win_l, int win_r, float softcap, int num_splits,
+                           void *workspace, size_t workspace_bytes, attn_stream_t stream) {
+  attn_status st = check_common(dtype, hq, hkv, d, scale, win_l, win_r, causal, softcap);
+  if (st != ATTN_OK) return st;
+  if (batch < 0 || total_q < 0 || num_splits < 0) return ATTN_ERR_INVALID;
+  if (!stride_ok(q_row_stride, hq, d)) return ATTN_ERR_INVALID;
+  if (batch == 0 || total_q == 0) return ATTN_OK;
+  st = check_cache(block_table, num_pages, page_size, max_pages_per_seq, batch, hkv, d,
+                   k_page_stride, v_page_stride);
+  if (st != ATTN_OK) return st;
+  if (!q || !out || !lse || !cu_seqlens_q || !cache_seqlens ||
+      (num_pages > 0 && (!k_cache || !v_cache)))
+    return ATTN_ERR_INVALID;
+  for (const void *p : {q, k_cache, v_cache, (const void *)out, (const void *)workspace})
+    if (!aligned16(p)) return ATTN_ERR_INVALID;
+  if ((int64_t)total_q * hq > INT32_MAX || hq > 65535) return ATTN_ERR_UNSUPPORTED;
+  const size_t need = attn_fwd_paged_workspace_size(batch, total_q, hq, hkv, d, num_splits);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
+  const DeviceInfo *di = device_info();
+  if (!di) return ATTN_ERR_CUDA;
+  const int64_t page_elems = (int64_t)page_size * hkv * d;
+  PagedArgs a{};
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.o = out;
+  a.lse = lse;
+  a.cu_q = cu_seqlens_q;
+  a.cache_seqlens = cache_seqlens;
+  a.block_table = block_table;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages_per_seq;
+  a.q_rs = q_row_stride ? q_row_stride : (int64_t)hq * d;
+  a.k_ps = k_page_stride ? k_page_stride : page_elems;
+  a.v_ps = v_page_stride ? v_page_stride : page_elems;
+  a.appended = appended != 0;
+  a.batch = batch;
+  a.total_q = total_q;
+  a.dtype = dtype;
+  a.hq = hq;
+  a.hkv = hkv;
+  a.d = d;
+  a.scale = scale;
+  a.softcap = softcap > 0.f ? softcap : 0.f;
+  a.win_l = win_l;
+  a.win_r = win_r;
+  a.err = di->err;
+  a.wait_ns = wait_limit_ns();
+  a.stall = test_stall();
+  return launched(launch_paged_simt(a, stream));
+}
+
+uint64_t attn_rope_phase(double inv_freq) {
+  // the fraction of a turn per position, scaled by 2^64 in two exact steps
+  // (a fraction that rounds up to a whole turn is phase 0)
+  const double turns = inv_freq / 6.283185307179586476925;
+  const double frac = turns - floor(turns);
+  const double hi = floor(ldexp(frac, 32));
+  const double lo = rint(ldexp(ldexp(frac, 32) - hi, 32));
+  return ((uint64_t)hi << 32) + (uint64_t)lo;
+}
+
+attn_status attn_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out,
+                              int64_t q_row_stride, int64_t k_row_stride,
+                              int64_t q_out_row_stride, int64_t k_out_row_stride,
+                              const void *q_weight, const void *k_weight, float eps,
+                              const uint64_t *phases, int rot, int interleaved,
+                              const int32_t *positions, int dtype, int b, int s, int hq, int hkv,
+                              int d, attn_stream_t stream) {
+  attn_status st = check_rope(dtype, hq, hkv, d, q_weight, k_weight, eps, phases, rot);
+  if (st != ATTN_OK) return st;
+  if (b < 0 || s < 0) return ATTN_ERR_INVALID;
+  if (!stride_ok(q_row_stride, hq, d) || !stride_ok(k_row_stride, hkv, d) ||
+      !stride_ok(q_out_row_stride, hq, d) || !stride_ok(k_out_row_stride, hkv, d))
+    return ATTN_ERR_INVALID;
+  if (b == 0 || s == 0 || (hq == 0 && hkv == 0)) return ATTN_OK;
+  if ((hq > 0 && (!q || !q_out)) || (hkv > 0 && (!k || !k_out))) return ATTN_ERR_INVALID;
+  for (const void *p : {q, k, (const void *)q_out, (const void *)k_out})
+    if (!aligned16(p)) return ATTN_ERR_INVALID;
+  if ((int64_t)b * s > INT32_MAX / 64) return ATTN_ERR_UNSUPPORTED;
+  RopeArgs a{};
+  a.q = q;
+  a.k = k;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.q_rs = q_row_stride ? q_row_stride : (int64_t)hq * d;
+  a.k_rs = k_row_stride ? k_row_stride : (int64_t)hkv * d;
+  a.q_out_rs = q_out_row_stride ? q_out_row_stride : (int64_t)hq * d;
+  a.k_out_rs = k_out_row_stride ? k_out_row_stride : (int64_t)hkv * d;
+  // in place needs the rows in the same places
+  if ((hq > 0 && q == q_out && a.q_rs != a.q_out_rs) ||
+      (hkv > 0 && k == k_out && a.k_rs != a.k_out_rs))
+    return ATTN_ERR_INVALID;
+  const DeviceInfo *di = device_info();
+  if (!di) return ATTN_ERR_CUDA;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = eps;
+  a.phases = phases;
+  a.rot = rot;
+  a.interleaved = interleaved != 0;
+  a.positions = positions;
+  a.rows = b * s;
+  a.s = s;
+  a.dtype = dtype;
+  a.hq = hq;
+  a.hkv = hkv;
+  a.d = d;
+  return launched(launch_norm_rope(a, di->sms, stream));
+}
+
+size_t attn_qk_norm_rope_bwd_workspace_size(int b, int s, int hq, int hkv, int d) {
+  if (b <= 0 || s <= 0 || hq + hkv <= 0 || d <= 0) return 0;
+  const DeviceInfo *di = device_info();
+  return align256(sizeof(float) * 2 * (size_t)d * rope_bwd_blocks(di ? di->sms : 152));
+}
+
+attn_status attn_qk_norm_rope_bwd(const void *q, const void *k, const void *dq_out,
+                                  const void *dk_out, void *dq, void *dk, int64_t q_row_stride,
+                                  int64_t k_row_stride, int64_t dq_row_stride,
+                                  int64_t dk_row_stride, const void *q_weight,
+                                  const void *k_weight, void *dq_weight, void *dk_weight,
+                                  float eps, const uint64_t *phases, int rot, int interleaved,
+                                  const int32_t *positions, int dtype, int b, int s, int hq,
+                                  int hkv, int d, void *workspace, size_t workspace_bytes,
+                                  attn_stream_t stream) {
+  attn_status st = check_rope(dtype, hq, hkv, d, q_weight, k_weight, eps, phases, rot);
+  if (st != ATTN_OK) return st;
+  if (b < 0 || s < 0) return ATTN_ERR_INVALID;
+  if (!stride_ok(q_row_stride, hq, d) || !stride_ok(k_row_stride, hkv, d) ||
+      !stride_ok(dq_row_stride, hq, d) || !stride_ok(dk_row_stride, hkv, d))
+    return ATTN_ERR_INVALID;
+  if ((hq > 0 && q_weight && !dq_weight) || (hkv > 0 && k_weight && !dk_weight))
+    return ATTN_ERR_INVALID;
+  if (hq == 0 && hkv == 0) return ATTN_OK;
+  if (b > 0 && s > 0) {
+    if ((hq > 0 && (!dq_out || !dq || (q_weight && !q))) ||
+        (hkv > 0 && (!dk_out || !dk || (k_weight && !k))))
+      return ATTN_ERR_INVALID;
+  }
+  for (const void *p : {q, k, dq_out, dk_out, (const void *)dq, (const void *)dk,
+                        (const void *)dq_weight, (const void *)dk_weight, (const void *)workspace})
+    if (!aligned16(p)) return ATTN_ERR_INVALID;
+  if ((int64_t)b * s > INT32_MAX / 64) return ATTN_ERR_UNSUPPORTED;
+  const size_t need = attn_qk_norm_rope_bwd_workspace_size(b, s, hq, hkv, d);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
+  RopeArgs a{};
+  a.q = q;
+  a.k = k;
+  a.gq = dq_out;
+  a.gk = dk_out;
+  a.q_out = dq;
+  a.k_out = dk;
+  a.q_rs = q_row_stride ? q_row_stride : (int64_t)hq * d;
+  a.k_rs = k_row_stride ? k_row_stride : (int64_t)hkv * d;
+  a.q_out_rs = dq_row_stride ? dq_row_stride : (int64_t)hq * d;
+  a.k_out_rs = dk_row_stride ? dk_row_stride : (int64_t)hkv * d;
+  a.gq_rs = (int64_t)hq * d;
+  a.gk_rs = (int64_t)hkv * d;
+  // in place needs the rows in the same places
+  if ((hq > 0 && dq == dq_out && a.q_out_rs != a.gq_rs) ||
+      (hkv > 0 && dk == dk_out && a.k_out_rs != a.gk_rs) ||
+      (hq > 0 && dq == q && a.q_out_rs != a.q_rs) || (hkv > 0 && dk == k && a.k_out_rs != a.k_rs))
+    return ATTN_ERR_INVALID;
+  const DeviceInfo *di = device_info();
+  if (!di) return ATTN_ERR_CUDA;
+  a.q_weight = hq > 0 ? q_weight : nullptr;
+  a.k_weight = hkv > 0 ? k_weight : nullptr;
+  a.q_gw = a.q_weight ? dq_weight : nullptr;
+  a.k_gw = a.k_weight ? dk_weight : nullptr;
+  a.gw_part = static_cast<float *>(workspace);
+  a.eps = eps;
+  a.phases = phases;
+  a.rot = rot;
+  a.interleaved = interleaved != 0;
+  a.positions = positions;
+  a.rows = b * s;
+  a.s = s;
+  a.dtype = dtype;
+  a.hq = hq;
+  a.hkv = hkv;
+  a.d = d;
+  return launched(launch_norm_rope_bwd(a, di->sms, stream));
+}
+
+attn_status attn_kvcache_append(const void *q, void *q_out, const void *k_new, const void *v_new,
+                                int64_t q_row_stride, int64_t k_row_stride, int64_t v_row_stride,
+                                void *k_cache, void *v_cache, int64_t k_page_stride,
+                                int64_t v_page_stride, const int32_t *cu_seqlens,
+                                const int32_t *cache_seqlens, const int32_t *block_table,
+                                int num_pages, int page_size, int max_pages_per_seq,
+                                const void *q_weight, const void *k_weight, float eps,
+                                const uint64_t *phases, int rot, int interleaved, int dtype,
+                                int batch, int total, int hq, int hkv, int d,
+                                attn_stream_t stream) {
+  attn_status st = check_rope(dtype, hq, hkv, d, q_weight, k_weight, eps, phases, rot);
+  if (st != ATTN_OK) return st;
+  if (batch < 0 || total < 0 || hkv == 0) return ATTN_ERR_INVALID;
+  if (!stride_ok(q_row_stride, hq, d) || !stride_ok(k_row_stride, hkv, d) ||
+      !stride_ok(v_row_stride, hkv, d))
+    return ATTN_ERR_INVALID;
+  if (batch == 0 || total == 0) return ATTN_OK;
+  st = check_cache(block_table, num_pages, page_size, max_pages_per_seq, batch, hkv, d,
+                   k_page_stride, v_page_stride);
+  if (st != ATTN_OK) return st;
+  if ((hq > 0 && (!q || !q_out)) || !k_new || !v_new || !cu_seqlens || !cache_seqlens ||
+      (num_pages > 0 && (!k_cache || !v_cache)))
+    return ATTN_ERR_INVALID;
+  for (const void *p : {q, (const void *)q_out, k_new, v_new, (const void *)k_cache,
+                        (const void *)v_cache})
+    if (!aligned16(p)) return ATTN_ERR_INVALID;
+  if (total > INT32_MAX / 64) return ATTN_ERR_UNSUPPORTED;
+  RopeArgs a{};
+  a.q = q;
+  a.k = k_new;
+  a.v = v_new;
+  a.q_out = q_out;
+  a.k_out = k_cache;
+  a.v_out = v_cache;
+  a.q_rs = q_row_stride ? q_row_stride : (int64_t)hq * d;
+  a.k_rs = k_row_stride ? k_row_stride : (int64_t)hkv * d;
+  a.v_rs = v_row_stride ? v_row_stride : (int64_t)hkv * d;
+  a.q_out_rs = (int64_t)hq * d;
+  const int64_t page_elems = (int64_t)page_size * hkv * d;
+  a.k_out_rs = k_page_stride ? k_page_stride : page_elems;
+  a.v_out_rs = v_page_stride ? v_page_stride : page_elems;
+  if (hq > 0 && q == q_out && a.q_rs != a.q_out_rs) return ATTN_ERR_INVALID;
+  const DeviceInfo *di = device_info();
+  if (!di) return ATTN_ERR_CUDA;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = eps;
+  a.phases = phases;
+  a.rot = rot;
+  a.interleaved = interleaved != 0;
+  a.rows = total;
+  a.s = total;
+  a.dtype = dtype;
+  a.hq = hq;
+  a.hkv = hkv;
+  a.d = d;
+  a.cu_seqlens = cu_seqlens;
+  a.cache_seqlens = cache_seqlens;
+  a.block_table = block_table;
+  a.batch = batch;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages_per_seq;
+  a.err = di->err;
+  return launched(launch_norm_rope(a, di->sms, stream));
 }
 
 attn_status attn_kvcache_advance(int32_t *cache_seqlens, int b, int s_new, attn_stream_t stream) {

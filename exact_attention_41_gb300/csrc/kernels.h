@@ -71,6 +71,48 @@ struct DecodeArgs {
   int stall;                    // test hook, as FwdArgs::stall
 };
 
+// Attention of ragged new tokens over a paged cache (attn_fwd_paged).
+struct PagedArgs {
+  const void *q, *k_cache, *v_cache;
+  void *o;
+  float *lse;                   // (hq, total_q)
+  const int32_t *cu_q;          // (batch + 1) offsets into the packed query rows
+  const int32_t *cache_seqlens, *block_table;  // block_table nullptr: one page per sequence
+  int num_pages, page_size, max_pages;
+  int64_t q_rs;                 // elements between consecutive query rows
+  int64_t k_ps, v_ps;           // elements between consecutive pages
+  int appended;                 // the chunk's own keys are in the cache behind cache_seqlens
+  int batch, total_q, dtype, hq, hkv, d;
+  float scale, softcap;         // softcap <= 0: off
+  int win_l, win_r;             // -1 = unbounded; causal already folded into win_r = 0
+  int *err;
+  uint64_t wait_ns;             // wall-clock limit of a device-side wait (ns)
+  int stall;                    // test hook, as FwdArgs::stall
+};
+
+// Per-head norm and rotation (attn_qk_norm_rope, its backward, and
+// attn_kvcache_append).  *_rs: elements between consecutive token rows; for
+// the append k_out_rs and v_out_rs are the page strides of the caches.
+struct RopeArgs {
+  const void *q, *k, *v;        // v: append only
+  void *q_out, *k_out, *v_out;  // backward: gradients of q and k
+  const void *gq, *gk;          // backward: gradients of the outputs
+  int64_t q_rs, k_rs, v_rs, q_out_rs, k_out_rs, v_out_rs, gq_rs, gk_rs;
+  const void *q_weight, *k_weight;  // nullptr: no norm
+  void *q_gw, *k_gw;                // backward: gradients of the weights
+  float *gw_part;                   // backward: workspace (blocks, 2, d) fp32
+  float eps;
+  const uint64_t *phases;       // (rot / 2) turns per position in 2^-64 turns
+  int rot, interleaved;
+  const int32_t *positions;     // (rows), or nullptr: row % s
+  int rows, s, dtype, hq, hkv, d;
+  int parts;                    // warps per token, set by the launcher
+  // append only
+  const int32_t *cu_seqlens, *cache_seqlens, *block_table;
+  int batch, num_pages, page_size, max_pages;
+  int *err;
+};
+
 // cuTensorMapEncodeTiled from the driver (looked up once), or nullptr.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 // 3-D (rows, heads, d) tensor map, box {64, box_heads, box_rows}, 128-byte
@@ -143,6 +185,12 @@ cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t st);
 cudaError_t launch_widen_e4m3(const void *src, void *dst, int64_t n, int sms, cudaStream_t st);
 // Debug probability matrix p (b, hq, sq, sk) fp32 from q, k and a.lse.
 cudaError_t launch_probs(const FwdArgs &a, float *p, cudaStream_t st);
+cudaError_t launch_paged_simt(const PagedArgs &a, cudaStream_t st);
+// Forward of the norm and rotation, or the append when a.cu_seqlens is set.
+cudaError_t launch_norm_rope(const RopeArgs &a, int sms, cudaStream_t st);
+cudaError_t launch_norm_rope_bwd(const RopeArgs &a, int sms, cudaStream_t st);
+// Most blocks of the backward, each of which writes 2 * d floats of workspace.
+int rope_bwd_blocks(int sms);
 // cache_seqlens[i] += s_new for i < b.
 cudaError_t launch_kvcache_advance(int32_t *cache_seqlens, int b, int s_new, cudaStream_t st);
 

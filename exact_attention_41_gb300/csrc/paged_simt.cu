@@ -1,0 +1,130 @@
+// Attention of a ragged chunk of new tokens over a paged cache on the CUDA
+// cores: one warp per query row and head, any page size.
+//
+// Per row: 32 keys at a time, one key per lane for the scores (a D-long dot
+// product each), the running maximum and sum of the softmax across the warp,
+// then D / 32 output columns per lane.  The work is bound by the dot products
+// on the FMA pipe.
+#include "paged.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kWarps = 4;
+
+// grid (ceil(total_q / kWarps), hq)
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32) paged_rows_kernel(const PagedArgs a) {
+  constexpr int V = D / 32;
+  __shared__ float qs[kWarps][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.x * kWarps + warp, h = blockIdx.y;
+  if (row >= a.total_q) return;
+  // sequence = how many sequences end at or before the row
+  int seq = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    const bool ended = b0 + lane < a.batch && a.cu_q[b0 + lane + 1] <= row;
+    seq += __popc(__ballot_sync(0xffffffffu, ended));
+  }
+  if (seq >= a.batch) return;  // behind the last sequence: left as it was
+  const PagedSeq s = paged_seq(a, seq);
+  if (s.err && lane == 0) raise_error(a.err, s.err);
+  const int i = row - s.q0;
+  if (i < 0 || i >= s.lq) return;
+  const int kvh = h / (a.hq / a.hkv);
+  const T *q = static_cast<const T *>(a.q) + (int64_t)row * a.q_rs + (int64_t)h * D;
+  for (int c = lane; c < D; c += 32) qs[warp][c] = Elem<T>::to_f(q[c]);
+  __syncwarp();
+  int lo, hi;
+  key_range(i, s.lq, s.lk, a.win_l, a.win_r, lo, hi);
+  float m = -INFINITY, l = 0.f, acc[V];
+#pragma unroll
+  for (int u = 0; u < V; ++u) acc[u] = 0.f;
+  bool bad = false;
+  for (int j0 = lo; j0 <= hi; j0 += 32) {
+    const int j = j0 + lane;
+    float x = -INFINITY;
+    int page = 0, slot = 0;
+    bool miss = false;
+    if (j <= hi) {
+      page = paged_page(a, seq, j / a.page_size);
+      slot = j % a.page_size;
+      miss = page < 0;
+    }
+    if (__any_sync(0xffffffffu, miss)) {
+      if (lane == 0) raise_error(a.err, kErrPageOutOfRange);
+      bad = true;
+      break;
+    }
+    if (j <= hi) {
+      const T *k = static_cast<const T *>(a.k_cache) + (int64_t)page * a.k_ps +
+                   ((int64_t)slot * a.hkv + kvh) * D;
+      float dot = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < D; c += 8) {
+        float e[8];
+        load_vec<T, 8>(k + c, e);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) dot = fmaf(qs[warp][c + u], e[u], dot);
+      }
+      x = dot * a.scale;
+      if (a.softcap > 0.f) x = a.softcap * tanhf(x / a.softcap);
+      x *= kLog2e;
+    }
+    const float m_new = fmaxf(m, warp_max(x));
+    // a row of -inf scores (a -inf query or key) has no finite maximum yet
+    const float m_use = m_new == -INFINITY ? 0.f : m_new;
+    const float alpha = exp2f(m - m_use);
+    const float p = exp2f(x - m_use);
+    l = l * alpha + warp_sum(p);
+#pragma unroll
+    for (int u = 0; u < V; ++u) acc[u] *= alpha;
+    const int n = min(32, hi - j0 + 1);
+    for (int jj = 0; jj < n; ++jj) {
+      const float pj = __shfl_sync(0xffffffffu, p, jj);
+      const int pg = __shfl_sync(0xffffffffu, page, jj), sl = __shfl_sync(0xffffffffu, slot, jj);
+      const T *v = static_cast<const T *>(a.v_cache) + (int64_t)pg * a.v_ps +
+                   ((int64_t)sl * a.hkv + kvh) * D;
+      float e[V];
+      load_vec<T, V>(v + lane * V, e);
+#pragma unroll
+      for (int u = 0; u < V; ++u) acc[u] = fmaf(pj, e[u], acc[u]);
+    }
+    m = m_new;
+  }
+  if (bad) {  // a page outside the pool: the result of an empty key set
+    l = 0.f;
+#pragma unroll
+    for (int u = 0; u < V; ++u) acc[u] = 0.f;
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int u = 0; u < V; ++u) acc[u] *= inv;
+  store_vec<T, V>(static_cast<T *>(a.o) + ((int64_t)row * a.hq + h) * D + lane * V, acc);
+  if (lane == 0)
+    a.lse[(int64_t)h * a.total_q + row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+template <typename T, int D>
+cudaError_t rows(const PagedArgs &a, cudaStream_t st) {
+  const int64_t gx = ((int64_t)a.total_q + kWarps - 1) / kWarps;
+  debug_log("paged: paged_rows_kernel (CUDA cores, one warp per query row and head) d=%d, %d rows x %d heads",
+            D, a.total_q, a.hq);
+  paged_rows_kernel<T, D><<<dim3((unsigned)gx, a.hq), kWarps * 32, 0, st>>>(a);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_simt(const PagedArgs &a, cudaStream_t st) {
+  const bool bf = a.dtype == ATTN_BF16;
+  switch (a.d) {
+    case 64: return bf ? rows<__nv_bfloat16, 64>(a, st) : rows<__half, 64>(a, st);
+    case 128: return bf ? rows<__nv_bfloat16, 128>(a, st) : rows<__half, 128>(a, st);
+    case 256: return bf ? rows<__nv_bfloat16, 256>(a, st) : rows<__half, 256>(a, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace attn

@@ -25,6 +25,7 @@ STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported configuration",
           6: "device-side data check failed"}
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_i64 = ctypes.c_int64
 _SIGS = {
     "attn_version": ([], ctypes.c_char_p),
     "attn_status_str": ([_i], ctypes.c_char_p),
@@ -46,6 +47,17 @@ _SIGS = {
                                  [_f, _i, _i, _i, _f, _i, _vp], _i),
     "attn_fwd_fp8_workspace_size": ([_i] * 4, _sz),
     "attn_fwd_fp8": ([_vp] * 5 + [_f] * 3 + [_i] * 6 + [_f, _i, _i, _i, _f, _vp, _sz, _vp], _i),
+    "attn_fwd_paged_workspace_size": ([_i] * 6, _sz),
+    "attn_fwd_paged": ([_vp] * 5 + [_i64] * 3 + [_vp] * 3 + [_i] * 10 +
+                       [_f, _i, _i, _i, _f, _i, _vp, _sz, _vp], _i),
+    "attn_rope_phase": ([ctypes.c_double], ctypes.c_uint64),
+    "attn_qk_norm_rope": ([_vp] * 4 + [_i64] * 4 + [_vp, _vp, _f, _vp, _i, _i, _vp] + [_i] * 6 +
+                          [_vp], _i),
+    "attn_qk_norm_rope_bwd_workspace_size": ([_i] * 5, _sz),
+    "attn_qk_norm_rope_bwd": ([_vp] * 6 + [_i64] * 4 + [_vp] * 4 + [_f, _vp, _i, _i, _vp] +
+                              [_i] * 6 + [_vp, _sz, _vp], _i),
+    "attn_kvcache_append": ([_vp] * 4 + [_i64] * 3 + [_vp] * 2 + [_i64] * 2 + [_vp] * 3 +
+                            [_i] * 3 + [_vp, _vp, _f, _vp] + [_i] * 8 + [_vp], _i),
     "attn_fwd_probs": ([_vp] * 4 + [_i] * 7 + [_f, _i, _i, _i, _f, _vp], _i),
     "attn_kvcache_advance": ([_vp, _i, _i, _vp], _i),
     "attn_get_device_error": ([_vp, ctypes.POINTER(_i)], _i),
@@ -398,3 +410,270 @@ def fwd_fp8(q, k, v, descale_q=1.0, descale_k=1.0, descale_v=1.0, *, scale=None,
                             _p(workspace), workspace.numel(), _stream())
     _check(st, "attn_fwd_fp8")
     return out, lse
+
+
+# ------------------------------------------- ragged chunks over a paged cache
+
+def _on_device(*ts):
+    """The tensors lie on one CUDA device; a guard that makes it current (the
+    calls below then run on that device's current stream)."""
+    torch = _torch()
+    ts = [t for t in ts if t is not None]
+    for t in ts:
+        _need(t.is_cuda, "tensors must be on a CUDA device")
+        _need(t.device == ts[0].device, "tensors must be on one device")
+    return torch.cuda.device(ts[0].device)
+
+
+def _like(t, ref, shape, what):
+    _need(t.dtype == ref.dtype, f"{what} must have the dtype of the queries or keys")
+    _need(tuple(t.shape) == tuple(shape), f"{what} must have shape {tuple(shape)}")
+
+
+def _packed_stride(t):
+    """Row stride (elements) of a (rows, h, d) tensor with dense heads; 0 when
+    contiguous."""
+    if t is None or t.is_contiguous():
+        return 0
+    rows, h, d = t.shape
+    _need(t.stride(2) == 1 and (h == 1 or t.stride(1) == d),
+          "a non-contiguous q/k/v must be a token-strided view with dense heads")
+    return 0 if rows <= 1 else t.stride(0)
+
+
+def _page_stride(t):
+    """Page stride (elements) of a (num_pages, page_size, hkv, d) pool whose
+    pages are dense; 0 when contiguous."""
+    if t.is_contiguous():
+        return 0
+    n, ps, h, d = t.shape
+    _need(t.stride(3) == 1 and (h == 1 or t.stride(2) == d) and (ps == 1 or t.stride(1) == h * d),
+          "the pages of a cache must be dense; only the page stride may be larger")
+    return 0 if n <= 1 else t.stride(0)
+
+
+def _cache_args(k_cache, v_cache, cu_seqlens, cache_seqlens, block_table):
+    _need(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype,
+          "k_cache and v_cache must be (num_pages, page_size, hkv, d) of one dtype")
+    batch = cache_seqlens.numel()
+    _need(cu_seqlens.dtype == _torch().int32 and cache_seqlens.dtype == _torch().int32,
+          "cu_seqlens and cache_seqlens must be int32")
+    _need(cu_seqlens.numel() == batch + 1, "cu_seqlens must have one entry more than cache_seqlens")
+    num_pages, page_size = k_cache.shape[:2]
+    max_pages = 1
+    if block_table is not None:
+        _need(block_table.dtype == _torch().int32 and block_table.dim() == 2 and
+              block_table.shape[0] == batch, "block_table must be int32 (batch, max_pages)")
+        max_pages = block_table.shape[1]
+    _cuda_contig(cu_seqlens, cache_seqlens, block_table)
+    return batch, num_pages, page_size, max_pages
+
+
+def paged_workspace(q, k_cache, batch, num_splits=0):
+    """Scratch memory of fwd_paged for these queries and this cache."""
+    torch = _torch()
+    rows, hq, d = q.shape
+    with _on_device(q):
+        n = lib().attn_fwd_paged_workspace_size(int(batch), rows, hq, k_cache.shape[2], d,
+                                                int(num_splits))
+    return torch.empty(max(n, 1), device=q.device, dtype=torch.uint8)
+
+
+def fwd_paged(q, k_cache, v_cache, cu_seqlens_q, cache_seqlens, *, block_table=None,
+              appended=True, scale=None, causal=False, window=(-1, -1), softcap=0.0,
+              num_splits=0, workspace=None, out=None, lse=None):
+    """Attention of a ragged chunk of new tokens over a paged cache.  q
+    (Tq,hq,d) -> out (Tq,hq,d), lse (hq,Tq) fp32; rows behind
+    cu_seqlens_q[-1] are left as they were.  appended: the chunk's keys are in
+    the cache already (kvcache_append), behind cache_seqlens tokens."""
+    torch = _torch()
+    rows, hq, d = q.shape
+    batch, num_pages, page_size, max_pages = _cache_args(k_cache, v_cache, cu_seqlens_q,
+                                                         cache_seqlens, block_table)
+    _need(k_cache.dtype == q.dtype and k_cache.shape[3] == d, "q and the cache must share dtype and d")
+    hkv = k_cache.shape[2]
+    out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
+    lse = torch.empty((hq, rows), device=q.device, dtype=torch.float32) if lse is None else lse
+    _like(out, q, q.shape, "out")
+    _need(tuple(lse.shape) == (hq, rows) and lse.dtype == torch.float32, "lse must be (hq, Tq) fp32")
+    ws = paged_workspace(q, k_cache, batch, num_splits) if workspace is None else workspace
+    strides = (_packed_stride(q), _page_stride(k_cache), _page_stride(v_cache))
+    _cuda_contig(out, lse, ws)
+    wl, wr = _win(window)
+    with _on_device(q, k_cache, v_cache, cu_seqlens_q, cache_seqlens, block_table, out, lse, ws):
+        st = lib().attn_fwd_paged(_p(q), _p(k_cache), _p(v_cache), _p(out), _p(lse), *strides,
+                                  _p(cu_seqlens_q), _p(cache_seqlens), _p(block_table), num_pages,
+                                  page_size, max_pages, int(bool(appended)), batch, rows, _dt(q),
+                                  hq, hkv, d, _scale(scale, d), int(bool(causal)), wl, wr,
+                                  float(softcap), int(num_splits), _p(ws),
+                                  ws.numel() * ws.element_size(), _stream())
+    _check(st, "attn_fwd_paged")
+    return out, lse
+
+
+# -------------------------------------------- per-head norm, position rotation
+
+def rope_phases(inv_freq, device=None):
+    """The phases of the rotation from its frequencies in radians per position
+    (a sequence or tensor of rot/2 numbers, read in 64 bits), as an int64
+    tensor on `device` (default: that of inv_freq, or the current CUDA device)."""
+    torch = _torch()
+    f = torch.as_tensor(inv_freq, dtype=torch.float64)
+    if device is None:
+        device = f.device if f.is_cuda else torch.device("cuda", torch.cuda.current_device())
+    bits = [lib().attn_rope_phase(float(x)) for x in f.flatten().cpu()]
+    _need(all(math.isfinite(float(x)) for x in f.flatten().cpu()), "frequencies must be finite")
+    return torch.tensor([b - (1 << 64) if b >= 1 << 63 else b for b in bits], dtype=torch.int64,
+                        device=device)
+
+
+def _rope_args(phases, q_weight, k_weight, ref):
+    """(phases pointer, rot) after the checks shared by the calls below."""
+    torch = _torch()
+    if phases is not None:
+        _need(phases.dtype == torch.int64 and phases.dim() == 1, "phases must be 1-D int64 (rope_phases)")
+        _need(2 * phases.numel() <= ref.shape[-1], "more rotation pairs than half of the head")
+        _cuda_contig(phases)
+    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _like(w, ref, (ref.shape[-1],), n)
+            _cuda_contig(w)
+    return _p(phases), 0 if phases is None else 2 * phases.numel()
+
+
+def _bshd(t):
+    """(b, s, h, d) sizes of a tensor, or zeros where there is none."""
+    _need(t is None or t.dim() == 4, "q and k must be (b, s, heads, d)")
+    return (0, 0, 0, 0) if t is None else tuple(t.shape)
+
+
+def _qk_sizes(q, k):
+    ref = q if q is not None else k
+    _need(ref is not None, "q or k is needed")
+    b, s, _, d = _bshd(ref)
+    for t in (q, k):
+        if t is not None:
+            _need(t.dtype == ref.dtype and _bshd(t)[:2] == (b, s) and t.shape[3] == d,
+                  "q and k must share batch, length, d and dtype")
+    return ref, b, s, _bshd(q)[2], _bshd(k)[2], d
+
+
+def _positions(positions, b, s):
+    if positions is not None:
+        _need(positions.dtype == _torch().int32 and positions.numel() == b * s,
+              "positions must be int32 with one entry per token")
+        _cuda_contig(positions)
+    return _p(positions)
+
+
+def qk_norm_rope(q, k, *, phases=None, positions=None, interleaved=False, q_weight=None,
+                 k_weight=None, eps=1e-6, q_out=None, k_out=None):
+    """Per-head RMS norm (where a weight is given) and position rotation (where
+    phases are, see rope_phases) of q (b,s,hq,d) and k (b,s,hkv,d) in one pass;
+    either may be None, token-strided views are taken, and q_out=q / k_out=k
+    works in place.  positions: int32 (b,s), default 0..s-1."""
+    torch = _torch()
+    ref, b, s, hq, hkv, d = _qk_sizes(q, k)
+    cf = torch.contiguous_format
+    if q is not None:
+        q_out = torch.empty_like(q, memory_format=cf) if q_out is None else q_out
+        _like(q_out, ref, q.shape, "q_out")
+    if k is not None:
+        k_out = torch.empty_like(k, memory_format=cf) if k_out is None else k_out
+        _like(k_out, ref, k.shape, "k_out")
+    ph, rot = _rope_args(phases, q_weight, k_weight, ref)
+    rs = [_row_stride(t) for t in (q, k, q_out, k_out)]
+    with _on_device(q, k, q_out, k_out, phases, positions, q_weight, k_weight):
+        st = lib().attn_qk_norm_rope(_p(q), _p(k), _p(q_out), _p(k_out), *rs, _p(q_weight),
+                                     _p(k_weight), float(eps), ph, rot, int(bool(interleaved)),
+                                     _positions(positions, b, s), _dt(ref), b, s, hq, hkv, d,
+                                     _stream())
+    _check(st, "attn_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd_workspace(q, k):
+    """Scratch memory of qk_norm_rope_bwd for these queries and keys."""
+    torch = _torch()
+    ref, b, s, hq, hkv, d = _qk_sizes(q, k)
+    with _on_device(ref):
+        n = lib().attn_qk_norm_rope_bwd_workspace_size(b, s, hq, hkv, d)
+    return torch.empty(max(n, 1), device=ref.device, dtype=torch.uint8)
+
+
+def qk_norm_rope_bwd(q, k, dq_out, dk_out, *, phases=None, positions=None, interleaved=False,
+                     q_weight=None, k_weight=None, eps=1e-6, workspace=None, dq=None, dk=None,
+                     dq_weight=None, dk_weight=None):
+    """Backward of qk_norm_rope -> dq, dk, dq_weight, dk_weight (None where the
+    forward had none).  dq / dk may be views of a packed gradient, or dq_out /
+    dk_out themselves."""
+    torch = _torch()
+    ref, b, s, hq, hkv, d = _qk_sizes(q, k)
+    _need((dq_out is None) == (q is None) and (dk_out is None) == (k is None),
+          "the gradients must be those of the forward's outputs")
+    cf = torch.contiguous_format
+    for t, g, n in ((q, dq_out, "dq_out"), (k, dk_out, "dk_out")):
+        if t is not None:
+            _like(g, ref, t.shape, n)
+    if q is not None:
+        dq = torch.empty_like(q, memory_format=cf) if dq is None else dq
+        _like(dq, ref, q.shape, "dq")
+    if k is not None:
+        dk = torch.empty_like(k, memory_format=cf) if dk is None else dk
+        _like(dk, ref, k.shape, "dk")
+    if q is not None and q_weight is not None and dq_weight is None:
+        dq_weight = torch.empty_like(q_weight)
+    if k is not None and k_weight is not None and dk_weight is None:
+        dk_weight = torch.empty_like(k_weight)
+    for w, n in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
+        if w is not None:
+            _like(w, ref, (d,), n)
+    ws = qk_norm_rope_bwd_workspace(q, k) if workspace is None else workspace
+    ph, rot = _rope_args(phases, q_weight, k_weight, ref)
+    _cuda_contig(dq_out, dk_out, dq_weight, dk_weight, ws)
+    rs = [_row_stride(t) for t in (q, k, dq, dk)]
+    with _on_device(q, k, dq_out, dk_out, dq, dk, phases, positions, q_weight, k_weight, dq_weight,
+                    dk_weight, ws):
+        st = lib().attn_qk_norm_rope_bwd(_p(q), _p(k), _p(dq_out), _p(dk_out), _p(dq), _p(dk), *rs,
+                                         _p(q_weight), _p(k_weight), _p(dq_weight), _p(dk_weight),
+                                         float(eps), ph, rot, int(bool(interleaved)),
+                                         _positions(positions, b, s), _dt(ref), b, s, hq, hkv, d,
+                                         _p(ws), ws.numel() * ws.element_size(), _stream())
+    _check(st, "attn_qk_norm_rope_bwd")
+    return dq, dk, dq_weight, dk_weight
+
+
+def kvcache_append(k_new, v_new, k_cache, v_cache, cu_seqlens, cache_seqlens, *, block_table=None,
+                   q=None, q_out=None, phases=None, interleaved=False, q_weight=None,
+                   k_weight=None, eps=1e-6):
+    """Appends k_new/v_new (T,hkv,d) of ragged new tokens to a paged cache at
+    the positions behind cache_seqlens, with the norm and rotation of the keys
+    on the way; q (T,hq,d), if given, is normed and rotated at the same
+    positions into q_out, which is returned.  Does not modify cache_seqlens."""
+    torch = _torch()
+    total, hkv, d = k_new.shape
+    batch, num_pages, page_size, max_pages = _cache_args(k_cache, v_cache, cu_seqlens,
+                                                         cache_seqlens, block_table)
+    _like(v_new, k_new, k_new.shape, "v_new")
+    _need(k_cache.dtype == k_new.dtype and tuple(k_cache.shape[2:]) == (hkv, d),
+          "the cache must have the heads, d and dtype of the new keys")
+    hq = 0
+    if q is not None:
+        hq = q.shape[1]
+        _like(q, k_new, (total, hq, d), "q")
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format) if q_out is None else q_out
+        _like(q_out, q, q.shape, "q_out")
+        _cuda_contig(q_out)
+    ph, rot = _rope_args(phases, q_weight, k_weight, k_new)
+    rs = [_packed_stride(t) for t in (q, k_new, v_new)]
+    with _on_device(k_new, v_new, k_cache, v_cache, cu_seqlens, cache_seqlens, block_table, q,
+                    q_out, phases, q_weight, k_weight):
+        st = lib().attn_kvcache_append(_p(q), _p(q_out) if q is not None else None, _p(k_new),
+                                       _p(v_new), *rs, _p(k_cache), _p(v_cache),
+                                       _page_stride(k_cache), _page_stride(v_cache),
+                                       _p(cu_seqlens), _p(cache_seqlens), _p(block_table),
+                                       num_pages, page_size, max_pages, _p(q_weight),
+                                       _p(k_weight), float(eps), ph, rot, int(bool(interleaved)),
+                                       _dt(k_new), batch, total, hq, hkv, d, _stream())
+    _check(st, "attn_kvcache_append")
+    return q_out if q is not None else None

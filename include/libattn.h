@@ -245,6 +245,143 @@ attn_status attn_fwd_kvcache_noalloc(const void *q, void *k_cache, void *v_cache
                                      attn_stream_t stream);
 
 /*
+ * Attention of a ragged chunk of new tokens over a paged cache (chunked
+ * prefill, mixed prefill and decode steps, drafted tokens; the pages have no
+ * counterpart beyond Q8, Q17 and Q18, which it joins).  q (total_q,hq,d), out
+ * (total_q,hq,d), lse (hq,total_q) fp32; sequence i owns the query rows
+ * cu_seqlens_q[i] .. cu_seqlens_q[i+1]-1 (DEVICE int32 array of batch+1
+ * offsets that never decrease; any of them may be empty).  Rows behind the
+ * last sequence are left as they were, so total_q may be a padded size.
+ *
+ * Keys: logical token t of sequence i lives in page
+ * block_table[i*max_pages_per_seq + t/page_size], slot t%page_size of the
+ * pools k_cache/v_cache (num_pages, page_size, hkv, d); *_page_stride is the
+ * number of elements from one page to the next (0: contiguous; a larger one
+ * takes pools that interleave K and V pages), a multiple of 8.  Only the
+ * table entries of pages that hold a key some row sees are read.  block_table
+ * == NULL: a contiguous cache of page_size tokens per sequence, num_pages =
+ * batch and max_pages_per_seq = 1.  page_size: any; multiples of 16 (and
+ * contiguous caches) run on the tensor cores.
+ *
+ * cache_seqlens (batch) int32 DEVICE array, read only.  appended != 0: the
+ * chunk's own keys and values are already in the cache behind cache_seqlens[i]
+ * tokens (attn_kvcache_append puts them there), so L_i = cache_seqlens[i] +
+ * sq_i; appended == 0: L_i = cache_seqlens[i] (keys of another origin, e.g. an
+ * encoder's states).  Masks align bottom-right as everywhere: row r of
+ * sequence i sits at position L_i - sq_i + r.
+ *
+ * What the cache holds in slots that no row of the call sees is never used,
+ * whatever it is (NaN too); visible keys and values must be finite.  A bad
+ * length (negative, or L_i above max_pages_per_seq * page_size) or page (outside
+ * [0, num_pages)) raises the device error word and gives the rows concerned
+ * the result of an empty key set, O = 0 and LSE = -inf (with several key
+ * ranges per row, the bad range counts as empty).
+ *
+ * q_row_stride: elements between consecutive query rows (0: hq * d), at least
+ * hq * d and a multiple of 8.  num_splits: 0 = choose on the device from the
+ * lengths; else the number of key ranges each row's keys are split into.  The
+ * result does not depend on it beyond rounding.  workspace: at least
+ * attn_fwd_paged_workspace_size(...) bytes, 256-byte aligned, contents
+ * arbitrary; calls that may run at the same time need one each.
+ */
+size_t attn_fwd_paged_workspace_size(int batch, int total_q, int hq, int hkv, int d,
+                                     int num_splits);
+
+attn_status attn_fwd_paged(const void *q, const void *k_cache, const void *v_cache, void *out,
+                           float *lse, int64_t q_row_stride, int64_t k_page_stride,
+                           int64_t v_page_stride, const int32_t *cu_seqlens_q,
+                           const int32_t *cache_seqlens, const int32_t *block_table,
+                           int num_pages, int page_size, int max_pages_per_seq, int appended,
+                           int batch, int total_q, int dtype, int hq, int hkv, int d, float scale,
+                           int causal, int win_l, int win_r, float softcap, int num_splits,
+                           void *workspace, size_t workspace_bytes, attn_stream_t stream);
+
+/*
+ * Position rotation and per-head norm (no counterpart on the pages; what
+ * stands between a projection and these attention calls).  For one head x of
+ * a token at position p:
+ *
+ *   z = weight * x / sqrt(mean(x^2) + eps)      (z = x when weight is NULL)
+ *   y = z with pair j of its first `rot` elements turned by p * f_j:
+ *       (a, b) -> (a cos - b sin, a sin + b cos)
+ *
+ * Pair j is (j, j + rot/2), or (2j, 2j + 1) when interleaved != 0.  The
+ * frequencies come as phases: DEVICE uint64 array of rot/2 values, 16-byte
+ * aligned, phases[j] = attn_rope_phase(f_j) = f_j / (2 pi) of a turn in units
+ * of 2^-64 turns, so that p * phases[j] mod 2^64 is the exact angle however
+ * far p is.  rot: a multiple of 16, 0 <= rot <= d; 0 turns nothing and phases
+ * may be NULL.  weight: d elements in dtype, shared by the heads; eps finite
+ * and >= 0.  Arithmetic is fp32, rounded once to dtype.
+ */
+
+/* The phase of a frequency in radians per position (finite).  Host only. */
+uint64_t attn_rope_phase(double inv_freq);
+
+/*
+ * Norm and rotation of q (b,s,hq,d) and k (b,s,hkv,d) into q_out and k_out of
+ * the same shapes, in one pass.  Token strides as in attn_fwd_strided (0:
+ * contiguous), so views of packed qkv tensors are read and written in place;
+ * q_out may be q and k_out k (with the same stride).  hq or hkv may be 0 with
+ * NULL pointers.  positions: DEVICE int32 (b*s), or NULL for 0 .. s-1 in every
+ * batch entry.
+ */
+attn_status attn_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out,
+                              int64_t q_row_stride, int64_t k_row_stride,
+                              int64_t q_out_row_stride, int64_t k_out_row_stride,
+                              const void *q_weight, const void *k_weight, float eps,
+                              const uint64_t *phases, int rot, int interleaved,
+                              const int32_t *positions, int dtype, int b, int s, int hq, int hkv,
+                              int d, attn_stream_t stream);
+
+/*
+ * Its gradient: q, k, weights, phases and positions as in the forward call,
+ * dq_out/dk_out the gradients of its outputs (contiguous).  Writes dq, dk
+ * (token strides as above; dq may be dq_out and dk dk_out when contiguous) and
+ * dq_weight, dk_weight (d elements in dtype, summed in fp32 over all tokens
+ * and heads in a fixed order: the same bits every run).  Without a weight the
+ * matching q or k is not read and may be NULL, and no weight gradient is
+ * written.  workspace: attn_qk_norm_rope_bwd_workspace_size(...) bytes,
+ * 256-byte aligned, contents arbitrary.
+ */
+size_t attn_qk_norm_rope_bwd_workspace_size(int b, int s, int hq, int hkv, int d);
+
+attn_status attn_qk_norm_rope_bwd(const void *q, const void *k, const void *dq_out,
+                                  const void *dk_out, void *dq, void *dk, int64_t q_row_stride,
+                                  int64_t k_row_stride, int64_t dq_row_stride,
+                                  int64_t dk_row_stride, const void *q_weight,
+                                  const void *k_weight, void *dq_weight, void *dk_weight,
+                                  float eps, const uint64_t *phases, int rot, int interleaved,
+                                  const int32_t *positions, int dtype, int b, int s, int hq,
+                                  int hkv, int d, void *workspace, size_t workspace_bytes,
+                                  attn_stream_t stream);
+
+/*
+ * Appends the keys and values of ragged new tokens to a paged cache, with the
+ * norm and rotation of the keys on the way, and (hq > 0) writes the normed and
+ * rotated queries of the same tokens: everything between the projections and
+ * attn_fwd_paged in one launch.  k_new/v_new (total,hkv,d), q and q_out
+ * (total,hq,d; q_out contiguous); token r of sequence i (row cu_seqlens[i] +
+ * r) goes to logical position p = cache_seqlens[i] + r, which is also its
+ * rotation's position.  Caches, page strides, block_table (or NULL), lengths
+ * and padding rows as in attn_fwd_paged; the page size may be any.  The slots
+ * written by one call must be distinct.  cache_seqlens is not changed.  A token
+ * whose page lies outside the pool, or whose position is past the table,
+ * raises the device error word and writes nothing to the cache (its query is
+ * still written); a bad cu_seqlens or cache_seqlens entry raises it and skips
+ * the token.
+ */
+attn_status attn_kvcache_append(const void *q, void *q_out, const void *k_new, const void *v_new,
+                                int64_t q_row_stride, int64_t k_row_stride, int64_t v_row_stride,
+                                void *k_cache, void *v_cache, int64_t k_page_stride,
+                                int64_t v_page_stride, const int32_t *cu_seqlens,
+                                const int32_t *cache_seqlens, const int32_t *block_table,
+                                int num_pages, int page_size, int max_pages_per_seq,
+                                const void *q_weight, const void *k_weight, float eps,
+                                const uint64_t *phases, int rot, int interleaved, int dtype,
+                                int batch, int total, int hq, int hkv, int d,
+                                attn_stream_t stream);
+
+/*
  * FP8 forward (Inference Cookbook FAQ Q20: FP8 inside, BF16 out; FAQ Q10
  * gives 1e-2 absolute / 1e-2 relative as the FP8 tolerance).  q (b,sq,hq,d)
  * and k, v (b,sk,hkv,d) hold OCP FP8 E4M3 bytes; the inputs they stand for

@@ -1,0 +1,268 @@
+"""Attention of a ragged chunk of new tokens over a paged cache, against the
+float64 oracle.
+
+Tolerance, from the arithmetic (h: half a step of the storage type, relative):
+the probabilities are rounded to the storage type before the product with V, so
+O moves by at most h sum_j P_j |v_j| = h A; the output rounds by h |O|.  A score
+is an fp32 sum of d products: at most d 2^-23 scale sum_i |q_i k_i| off, which
+for the inputs here (N(0,1), so sum |q_i k_i| < 0.9 d, scale = d^-1/2) is below
+d^1.5 2^-23 < 5e-4 at d = 256; P and the row sum each move by that much
+relative: 2 * 5e-4 A.  exp2 and the reciprocal add below 1e-5 A.  The LSE
+tolerance is the contract's 1e-3.
+"""
+import math
+
+import numpy as np
+import pytest
+
+from exact_attention_41_gb300 import synthetic as syn
+from oracle import serving
+from tests.helpers import assert_lse, dev, dev_i32, f64, host
+
+pytestmark = pytest.mark.gpu
+
+HALF = {syn.F16: 2.0 ** -11, syn.BF16: 2.0 ** -8}
+
+
+def make(seed, new, cached, hq, hkv, d, page, dtype, *, appended=True, pad=0, paged=True, win_l=-1,
+         poison=True):
+    """Inputs whose cache holds NaN in every slot that no row sees, and whose
+    table holds no page where no row sees a key."""
+    rng = np.random.default_rng(seed)
+    b = len(new)
+    length = [c + (n if appended else 0) for n, c in zip(new, cached)]
+    mk = lambda shape: syn.normal_bits(rng, shape, dtype)
+    nan = 0x7E00 if dtype == syn.F16 else 0x7FC0
+    total = sum(new) + pad
+    if paged:
+        need = [-(-n // page) for n in length]
+        width = max(max(need), 1) + 1
+        pool = sum(need) + 3
+        perm = rng.permutation(pool)
+        table = np.full((b, width), -9, np.int32)
+        at = 0
+        for i, n in enumerate(need):
+            table[i, :n] = perm[at:at + n]
+            at += n
+    else:
+        pool, table = b, None
+    kc, vc = mk((pool, page, hkv, d)), mk((pool, page, hkv, d))
+    if poison:
+        seen = np.zeros((pool, page), bool)
+        for i in range(b):
+            first = 0 if win_l < 0 else max(0, length[i] - new[i] - win_l)
+            for t in range(first if new[i] else length[i], length[i]):
+                seen[i if table is None else table[i, t // page], t % page] = True
+            if table is not None:
+                table[i, :first // page] = -7
+        kc[~seen], vc[~seen] = nan, nan
+    return dict(q=mk((total, hq, d)), kc=kc, vc=vc, table=table, cached=np.asarray(cached, np.int32),
+                cu=np.cumsum([0] + list(new)).astype(np.int32), dtype=dtype, appended=appended)
+
+
+def call(c, **kw):
+    from exact_attention_41_gb300 import libattn
+
+    dt = c["dtype"]
+    table = None if c["table"] is None else dev_i32(c["table"])
+    return libattn.fwd_paged(dev(c["q"], dt), dev(c["kc"], dt), dev(c["vc"], dt), dev_i32(c["cu"]),
+                             dev_i32(c["cached"]), block_table=table, appended=c["appended"], **kw)
+
+
+def want(c, kw):
+    dt = c["dtype"]
+    win = kw.get("window", (-1, -1))
+    d = c["q"].shape[2]
+    kc, vc = (np.nan_to_num(f64(c[n], dt)) for n in ("kc", "vc"))
+    return serving.paged_forward(f64(c["q"], dt), kc, vc, c["cu"], c["cached"], c["table"],
+                                 kw.get("scale", 1 / math.sqrt(d)), appended=c["appended"],
+                                 causal=kw.get("causal", False), win_l=win[0], win_r=win[1],
+                                 softcap=kw.get("softcap", 0.0))
+
+
+def check(c, o, lse, kw):
+    ro, rl, spread = want(c, kw)
+    n = int(c["cu"][-1])
+    got, h = host(o)[:n], HALF[c["dtype"]]
+    bound = h * np.abs(ro[:n]) + (h + 1.01e-3) * spread[:n] + 2.0 ** -24
+    err = np.abs(got - ro[:n])
+    assert np.isfinite(got).all()
+    assert (err <= bound).all(), f"worst err/bound {(err / bound).max():.3f}"
+    assert_lse(host(lse)[:, :n], rl[:, :n])
+
+
+def run(c, **kw):
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    libattn.device_error()
+    o, lse = call(c, **kw)
+    torch.cuda.synchronize()
+    assert libattn.device_error() == (0, 0)
+    check(c, o, lse, kw)
+    return o, lse
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 48, 128, 24])
+@pytest.mark.parametrize("splits", [0, 1, 3])
+def test_ragged_chunks(d, page, splits):
+    """Empty sequences, single tokens, chunks that end inside tiles and pages."""
+    c = make(1, [1, 0, 37, 130, 1, 5], [0, 40, 300, 65, 513, 11], 8, 2, d, page, syn.BF16)
+    run(c, causal=True, num_splits=splits)
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (4, 4), (10, 2), (7, 1), (12, 1), (48, 1), (100, 1),
+                                    (150, 1), (6, 2)])
+@pytest.mark.parametrize("new", [[1, 1, 1], [70, 3, 200]])
+def test_head_groups(hq, hkv, new):
+    """Groups that fill a tile, that leave a part of it empty, and larger ones."""
+    c = make(2, new, [100, 31, 0], hq, hkv, 64, 32, syn.F16)
+    run(c, causal=True)
+
+
+@pytest.mark.parametrize("dtype", [syn.F16, syn.BF16])
+@pytest.mark.parametrize("kw", [
+    dict(causal=True, window=(50, 0)), dict(window=(20, 9)), dict(window=(0, 0)),
+    dict(causal=True, softcap=5.0), dict(causal=True, window=(200, 0), softcap=2.0), dict(),
+    dict(window=(-1, 3)), dict(causal=True, scale=0.0),
+])
+def test_masks(dtype, kw):
+    c = make(3, [64, 1, 129, 300], [77, 600, 0, 33], 6, 3, 128, 16, dtype,
+             win_l=kw.get("window", (-1,))[0])
+    run(c, **kw)
+    run(c, num_splits=4, **kw)
+
+
+@pytest.mark.parametrize("splits", [0, 1, 2])
+def test_keys_of_another_origin_and_empty_rows(splits):
+    """appended = False: cached keys only.  With fewer keys than rows under a
+    causal mask the first rows see nothing: O = 0, LSE = -inf; so do all rows
+    of a sequence without keys."""
+    c = make(4, [40, 7, 3, 150], [300, 0, 2, 20], 8, 2, 64, 16, syn.BF16, appended=False)
+    run(c, num_splits=splits)
+    o, lse = run(c, causal=True, num_splits=splits)
+    assert (host(o)[40:47] == 0).all() and np.isneginf(host(lse)[:, 40:47]).all()
+
+
+def test_many_sequences():
+    """More sequences than a warp has lanes, most of one token, some empty."""
+    rng = np.random.default_rng(5)
+    new = [int(x) for x in rng.choice([0, 1, 1, 1, 2, 17], 150)]
+    cached = [int(x) for x in rng.integers(0, 400, 150)]
+    c = make(5, new, cached, 8, 2, 64, 16, syn.BF16)
+    for splits in (0, 1, 5):
+        run(c, causal=True, num_splits=splits)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_chunk_with_few_pages_seen(d):
+    """A chunk of 1500 rows (two tiles a block) behind 1000 tokens; then the same
+    under a window, with the pages before it gone."""
+    c = make(6, [1500], [1000], 8, 2, d, 64, syn.BF16)
+    run(c, causal=True)
+    c = make(6, [1500], [1000], 8, 2, d, 64, syn.BF16, win_l=300)
+    run(c, causal=True, window=(300, 0))
+
+
+def test_long_cache_of_one_sequence():
+    """One token against 20000 keys: the keys are split and the pieces joined."""
+    c = make(7, [1], [20000], 8, 1, 128, 16, syn.BF16)
+    for splits in (0, 1, 7, 64):
+        run(c, causal=True, num_splits=splits)
+
+
+@pytest.mark.parametrize("d", [64, 256])
+def test_contiguous_cache(d):
+    c = make(8, [9, 1, 0], [60, 0, 31], 4, 2, d, 69, syn.F16, paged=False)
+    run(c, causal=True)
+
+
+def test_strided_queries_interleaved_pools_and_padding_rows():
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    c = make(9, [20, 1, 33], [50, 200, 0], 8, 2, 128, 32, syn.BF16, pad=11)
+    n = int(c["cu"][-1])
+    args = (dev_i32(c["cu"]), dev_i32(c["cached"]))
+    kc, vc = dev(c["kc"], c["dtype"]), dev(c["vc"], c["dtype"])
+    pools = torch.stack([kc, vc], dim=1).contiguous()       # (pages, 2, page, hkv, d)
+    wide = torch.full((c["q"].shape[0], 12, 128), 5.0, device="cuda", dtype=torch.bfloat16)
+    wide[:, :8] = dev(c["q"], c["dtype"])
+    out = torch.full((c["q"].shape[0], 8, 128), 7.0, device="cuda", dtype=torch.bfloat16)
+    lse = torch.full((8, c["q"].shape[0]), 7.0, device="cuda")
+    libattn.fwd_paged(wide[:, :8], pools[:, 0], pools[:, 1], *args, block_table=dev_i32(c["table"]),
+                      causal=True, out=out, lse=lse)
+    o2, l2 = call(c, causal=True)
+    torch.cuda.synchronize()
+    assert torch.equal(out[:n], o2[:n]) and torch.equal(lse[:, :n], l2[:, :n])
+    assert (out[n:] == 7.0).all() and (lse[:, n:] == 7.0).all()
+    check(c, out, lse, dict(causal=True))
+
+
+def test_same_bits_every_run_and_any_workspace_contents():
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    c = make(10, [3, 1, 40], [2000, 5000, 100], 8, 2, 128, 16, syn.BF16)
+    q, kc = dev(c["q"], c["dtype"]), dev(c["kc"], c["dtype"])
+    runs = []
+    for fill in (0, 0xFF, 0x7F):
+        ws = libattn.paged_workspace(q, kc, 3, 6).fill_(fill)
+        runs.append(call(c, causal=True, num_splits=6, workspace=ws))
+    torch.cuda.synchronize()
+    for o, lse in runs[1:]:
+        assert torch.equal(o, runs[0][0]) and torch.equal(lse, runs[0][1])
+
+
+def test_bad_lengths_and_pages_give_empty_rows():
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    new, cached = [5, 9, 4], [100, 200, 50]
+    for splits in (1, 3):
+        for what, bit in (("page", 1), ("negative", 16), ("overflow", 2)):
+            c = make(11, new, cached, 8, 2, 128, 16, syn.BF16, poison=False)
+            good = dict(c, table=c["table"].copy(), cached=c["cached"].copy())
+            if what == "page":
+                c["table"][1, 3] = 10 ** 6
+            else:
+                c["cached"][1] = -4 if what == "negative" else 10 ** 6
+            libattn.device_error()
+            o, lse = call(c, causal=True, num_splits=splits)
+            torch.cuda.synchronize()
+            st, word = libattn.device_error()
+            assert st == 6 and word == bit, (what, st, word)
+            ro, rl, _ = want(good, dict(causal=True))
+            rows = [r for r in range(18) if not 5 <= r < 14]
+            np.testing.assert_allclose(host(o)[rows], ro[rows], atol=2e-2, rtol=2e-2)
+            if splits == 1 or what != "page":
+                assert (host(o)[5:14] == 0).all() and np.isneginf(host(lse)[:, 5:14]).all()
+            assert np.isfinite(host(o)).all()
+
+
+def test_offsets_out_of_order_or_past_the_rows():
+    """Such sequences are skipped and flagged; no row behind the tensors is touched."""
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    for cu in ([0, 5, 14, 19], [0, 5, 3, 18], [-2, 5, 14, 18]):
+        c = make(12, [5, 9, 4], [100, 200, 50], 8, 2, 128, 16, syn.BF16, poison=False)
+        c["cu"] = np.asarray(cu, np.int32)
+        guard = 4
+        dt = c["dtype"]
+        out = torch.full((18 + guard, 8, 128), 7.0, device="cuda", dtype=torch.bfloat16)
+        lse = torch.full((8 * 18 + guard,), 7.0, device="cuda")
+        libattn.device_error()
+        libattn.fwd_paged(dev(c["q"], dt), dev(c["kc"], dt), dev(c["vc"], dt), dev_i32(c["cu"]),
+                          dev_i32(c["cached"]), block_table=dev_i32(c["table"]), causal=True,
+                          out=out[:18], lse=lse[:8 * 18].view(8, 18))
+        torch.cuda.synchronize()
+        st, word = libattn.device_error()
+        assert st == 6 and word & 16, (cu, st, word)
+        assert (out[18:] == 7.0).all() and (lse[8 * 18:] == 7.0).all()

@@ -1,0 +1,374 @@
+"""Per-head norm with position rotation (forward and gradient) and the append
+to a paged cache, against the float64 oracle.
+
+Tolerances, from the arithmetic (h: half a step of the storage type, relative;
+u = 2^-24):
+* the angle is exact to 2^-32 turns, its fp32 value to pi u, sincospi to 2 u, so
+  a turned pair (a, b) is off by at most 10 u (|a| + |b|); the norm (16 adds a
+  thread, 4 across lanes, one reciprocal root, two products) adds 26 u |z|;
+  together below 64 u times the largest |z| of the head = Z.  |y| rounds by
+  h |y|:  |dy| <= h |y| + 64 u Z.
+* gradient: gz as above from gy (64 u G), then gx = r (gz w - xh mean(gz w xh));
+  every factor carries at most 32 u more, so |dgx| <= h |gx| + 128 u r W G (1 + X)
+  with W, X the largest |w|, |xh| of the head (mean |xh| <= 1).
+* weight gradient: at most n additions one after another of terms that are off
+  by 96 u each: h |gw| + (n + 96) u sum |gz xh|, with n below the number of
+  heads that one thread adds plus 64.
+Subnormal steps of fp16 add 2^-25 everywhere.
+"""
+import numpy as np
+import pytest
+
+from exact_attention_41_gb300 import synthetic as syn
+from oracle import serving
+from tests.helpers import dev, dev_i32, f64, host
+
+pytestmark = pytest.mark.gpu
+
+HALF = {syn.F16: 2.0 ** -11, syn.BF16: 2.0 ** -8}
+U = 2.0 ** -24
+TINY = 2.0 ** -25
+
+
+def freqs(rot, base=10000.0):
+    return base ** (-2.0 * np.arange(rot // 2) / max(rot, 1))
+
+
+def check(got, want, bound, what):
+    got = np.asarray(got, np.float64)
+    assert got.shape == want.shape, (what, got.shape, want.shape)
+    err = np.abs(got - want)
+    assert (err <= bound).all(), \
+        f"{what}: worst err/bound {np.max(err / bound):.3f}, max err {err.max():.3e}"
+
+
+def weights(rng, d, dtype):
+    bits = syn.round_bits((1 + 0.3 * rng.standard_normal(d)).astype(np.float32), dtype)
+    return dev(bits, dtype), f64(bits, dtype)
+
+
+def phases(rot):
+    from exact_attention_41_gb300 import libattn
+
+    return libattn.rope_phases(freqs(rot)) if rot else None
+
+
+CASES = [
+    # b, s, hq, hkv, d, rot, interleaved, norm, dtype
+    (2, 37, 8, 2, 128, 128, False, True, syn.BF16),
+    (2, 37, 8, 2, 128, 128, True, True, syn.F16),
+    (1, 1, 4, 4, 64, 64, False, True, syn.BF16),
+    (3, 65, 5, 1, 64, 32, False, True, syn.F16),      # half of a head turned, odd head count
+    (1, 130, 3, 3, 256, 256, True, False, syn.BF16),  # rotation alone
+    (1, 33, 7, 1, 256, 96, False, True, syn.F16),     # a part that is no power of two
+    (2, 19, 6, 2, 128, 0, False, True, syn.BF16),     # norm alone
+    (1, 700, 16, 2, 64, 16, True, True, syn.BF16),
+    (4, 513, 2, 1, 128, 64, True, False, syn.F16),
+]
+
+
+def case_data(seed, b, s, hq, hkv, d, dtype):
+    rng = np.random.default_rng(seed)
+    q, k = (syn.normal_bits(rng, (b, s, h, d), dtype) for h in (hq, hkv))
+    return rng, q, k
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_forward(case):
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    b, s, hq, hkv, d, rot, inter, normed, dtype = case
+    rng, q, k = case_data(5, b, s, hq, hkv, d, dtype)
+    (wq, wq64), (wk, wk64) = weights(rng, d, dtype), weights(rng, d, dtype)
+    if not normed:
+        wq = wk = wq64 = wk64 = None
+    pos = rng.integers(0, 1 << 20, (b, s))
+    for given in (False, True):
+        at = pos if given else np.broadcast_to(np.arange(s), (b, s))
+        out = libattn.qk_norm_rope(dev(q, dtype), dev(k, dtype), phases=phases(rot),
+                                   positions=dev_i32(pos) if given else None, interleaved=inter,
+                                   q_weight=wq, k_weight=wk, eps=1e-5)
+        torch.cuda.synchronize()
+        for x, w, got, what in ((q, wq64, out[0], "q"), (k, wk64, out[1], "k")):
+            x = f64(x, dtype).reshape(b * s, -1, d)
+            want = serving.norm_rope(x, at.reshape(-1), freqs(rot), w, 1e-5, inter)
+            z = np.abs(serving.norm(x, w, 1e-5)).max(-1, keepdims=True)
+            check(host(got).reshape(want.shape), want, HALF[dtype] * np.abs(want) + 64 * U * z + TINY, what)
+            if rot < d and not normed:
+                np.testing.assert_array_equal(host(got).reshape(want.shape)[..., rot:], x[..., rot:])
+
+
+def test_far_positions_keep_their_angles():
+    """Positions up to 2^31 - 1, and negative ones: the angle is exact modulo a turn."""
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    from fractions import Fraction
+
+    d, dtype = 64, syn.F16
+    pos = np.array([[0, 1, 2 ** 20 + 1, 2 ** 24 + 1, 2 ** 30 + 12345, 2 ** 31 - 1, -1, -(2 ** 31)]])
+    f = freqs(d)
+    x = np.zeros((1, pos.size, 1, d))
+    x[..., :d // 2] = 1.0
+    bits = syn.round_bits(x.astype(np.float32), dtype)
+    out, _ = libattn.qk_norm_rope(dev(bits, dtype), None, phases=libattn.rope_phases(f),
+                                  positions=dev_i32(pos))
+    torch.cuda.synchronize()
+    turn = 2 * Fraction("3.14159265358979323846264338327950288419716939937510")
+    want = np.zeros((pos.size, d))
+    for r, p in enumerate(pos[0]):
+        for j in range(d // 2):
+            t = Fraction(float(f[j])) / turn * int(p)
+            a = 2 * np.pi * float(t - (t.numerator // t.denominator))
+            want[r, j], want[r, j + d // 2] = np.cos(a), np.sin(a)
+    # phase rounding: the 53-bit quotient by 2 pi, below 2^-55 turns, times 2^31
+    bound = HALF[dtype] * np.abs(want) + 64 * U + TINY + 2 * np.pi * 2.0 ** (31 - 54)
+    check(host(out)[0, :, 0], want, bound, "far positions")
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_backward(case):
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    b, s, hq, hkv, d, rot, inter, normed, dtype = case
+    rng, q, k = case_data(6, b, s, hq, hkv, d, dtype)
+    gq, gk = (syn.normal_bits(rng, x.shape, dtype) for x in (q, k))
+    (wq, wq64), (wk, wk64) = weights(rng, d, dtype), weights(rng, d, dtype)
+    if not normed:
+        wq = wk = wq64 = wk64 = None
+    pos = rng.integers(0, 5000, (b, s))
+    args = dict(phases=phases(rot), positions=dev_i32(pos), interleaved=inter, q_weight=wq,
+                k_weight=wk, eps=1e-5)
+    ws = libattn.qk_norm_rope_bwd_workspace(dev(q, dtype), dev(k, dtype)).fill_(0xFF)  # NaNs
+    runs = [libattn.qk_norm_rope_bwd(dev(q, dtype), dev(k, dtype), dev(gq, dtype), dev(gk, dtype),
+                                     workspace=ws, **args) for _ in range(2)]
+    torch.cuda.synchronize()
+    for a, b2 in zip(*runs):
+        assert (a is None) == (not normed and b2 is None)
+        assert a is None or torch.equal(a, b2), "not the same bits every run"
+    for x, g, w, got, gotw, what in ((q, gq, wq64, runs[0][0], runs[0][2], "q"),
+                                     (k, gk, wk64, runs[0][1], runs[0][3], "k")):
+        x, g = (f64(t, dtype).reshape(b * s, -1, d) for t in (x, g))
+        gx, gw = serving.norm_rope_backward(x, g, pos.reshape(-1), freqs(rot), w, 1e-5, inter)
+        gz = serving.rotate(g, -pos.reshape(-1), freqs(rot), inter)
+        big = np.abs(gz).max(-1, keepdims=True)
+        if normed:
+            r = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + 1e-5)
+            xh = x * r
+            big = r * np.abs(w).max() * big * (1 + np.abs(xh).max(-1, keepdims=True))
+            n = 64 + x.shape[0] * x.shape[1]
+            check(host(gotw), gw, HALF[dtype] * np.abs(gw) +
+                  (n + 96) * U * np.abs(gz * xh).reshape(-1, d).sum(0) + TINY, what + " weight")
+        else:
+            assert gotw is None
+        check(host(got).reshape(gx.shape), gx, HALF[dtype] * np.abs(gx) + 128 * U * big + TINY, what)
+
+
+def test_gradient_against_differences():
+    """The library's own forward, moved by a step along the gradient's own
+    direction: the loss changes by step * |g|^2.  fp16, small eps."""
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    rng = np.random.default_rng(8)
+    b, s, h, d = 1, 64, 4, 64
+    ph = phases(d)
+    w = torch.ones(d, device="cuda", dtype=torch.float16)
+    x = dev(syn.normal_bits(rng, (b, s, h, d), syn.F16), syn.F16)
+    gy = dev(syn.normal_bits(rng, (b, s, h, d), syn.F16), syn.F16)
+    gx, _, gw, _ = libattn.qk_norm_rope_bwd(x, None, gy, None, phases=ph, q_weight=w)
+    step = 0.125
+
+    def loss(x, w):
+        y, _ = libattn.qk_norm_rope(x, None, phases=ph, q_weight=w)
+        return float((y.double() * gy.double()).sum())
+
+    for up, dn, x0, g in ((lambda t: loss(t, w), None, x, gx), (lambda t: loss(x, t), None, w, gw)):
+        unit = (g.double() / g.double().norm())
+        a, c = (x0.double() + step * unit).half(), (x0.double() - step * unit).half()
+        moved = float(((a.double() - c.double()) * g.double()).sum())
+        # rounding of y: h |y| per element, random signs over 16384 elements times
+        # |gy|: below 2^-11 * sqrt(16384) * 5 = 0.32 per evaluation; curvature
+        # |step|^3: below 1e-2
+        assert abs((up(a) - up(c)) - moved) < 0.02 * abs(moved) + 0.7, (up(a) - up(c), moved)
+
+
+def test_in_place_and_packed_views():
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    rng = np.random.default_rng(9)
+    b, s, h, d, dtype = 2, 45, 6, 128, syn.BF16
+    qkv = dev(syn.normal_bits(rng, (b, s, 3, h, d), dtype), dtype)
+    (wq, _), (wk, _) = weights(rng, d, dtype), weights(rng, d, dtype)
+    kw = dict(phases=phases(d), q_weight=wq, k_weight=wk)
+    want = libattn.qk_norm_rope(qkv[:, :, 0].contiguous(), qkv[:, :, 1].contiguous(), **kw)
+    v = qkv[:, :, 2].clone()
+    gq, gk = (dev(syn.normal_bits(rng, (b, s, h, d), dtype), dtype) for _ in range(2))
+    grads = libattn.qk_norm_rope_bwd(qkv[:, :, 0].contiguous(), qkv[:, :, 1].contiguous(), gq, gk, **kw)
+    dqkv = torch.full_like(qkv, 7.0)
+    packed = libattn.qk_norm_rope_bwd(qkv[:, :, 0], qkv[:, :, 1], gq, gk, dq=dqkv[:, :, 0],
+                                      dk=dqkv[:, :, 1], **kw)
+    assert torch.equal(packed[0], grads[0]) and torch.equal(packed[1], grads[1])
+    assert torch.equal(packed[2], grads[2]) and torch.equal(packed[3], grads[3])
+    assert (dqkv[:, :, 2] == 7.0).all()
+    q_view, k_view = qkv[:, :, 0], qkv[:, :, 1]
+    got = libattn.qk_norm_rope(q_view, k_view, q_out=q_view, k_out=k_view, **kw)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(qkv[:, :, 2], v)
+    # gradients over their inputs
+    g2 = libattn.qk_norm_rope_bwd(None, gk.clone(), None, gq, dk=None, **kw)
+    gq2 = gq.clone()
+    g3 = libattn.qk_norm_rope_bwd(None, gk, None, gq2, dk=gq2, **kw)
+    assert torch.equal(g3[1], g2[1]) and g3[1].data_ptr() == gq2.data_ptr()
+
+
+def test_empty_training_batch_has_zero_weight_gradients():
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    q = torch.zeros(0, 5, 4, 64, device="cuda", dtype=torch.bfloat16)
+    w = torch.ones(64, device="cuda", dtype=torch.bfloat16)
+    dw = torch.full_like(w, 3.0)
+    libattn.qk_norm_rope_bwd(q, None, q, None, q_weight=w, dq_weight=dw, phases=phases(64))
+    assert (dw == 0).all()
+
+
+def append_data(seed, new, cached, hq, hkv, d, page, dtype, pad=3):
+    rng = np.random.default_rng(seed)
+    total = sum(new) + pad
+    need = [-(-(c + n) // page) for n, c in zip(new, cached)]
+    width = max(need) + 1
+    table = np.full((len(new), width), -5, np.int32)  # unused entries are no pages
+    perm = rng.permutation(sum(need) + 2)
+    at = 0
+    for i, n in enumerate(need):
+        table[i, :n] = perm[at:at + n]
+        at += n
+    pool = (sum(need) + 2, page, hkv, d)
+    mk = lambda shape: syn.normal_bits(rng, shape, dtype)
+    return dict(rng=rng, total=total, cu=np.cumsum([0] + list(new)).astype(np.int32), table=table,
+                kc=mk(pool), vc=mk(pool), q=mk((total, hq, d)), k=mk((total, hkv, d)),
+                v=mk((total, hkv, d)))
+
+
+@pytest.mark.parametrize("new,cached,hq,hkv,d,page,rot,inter,normed,dtype", [
+    ([1] * 5, [0, 1, 15, 16, 200], 8, 2, 128, 16, 128, False, True, syn.BF16),
+    ([3, 0, 40, 1], [5, 7, 0, 63], 5, 1, 64, 16, 32, True, True, syn.F16),
+    ([17, 130], [0, 250], 4, 4, 256, 256, 256, False, False, syn.BF16),
+    ([9, 2, 2], [1, 0, 30], 14, 2, 128, 7, 0, False, True, syn.F16),   # odd pages, no rotation
+    ([1] * 70, list(range(70)), 4, 1, 64, 32, 64, False, True, syn.BF16),
+    ([600], [1000], 16, 8, 64, 48, 64, False, False, syn.BF16),
+])
+def test_append(new, cached, hq, hkv, d, page, rot, inter, normed, dtype):
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    c = append_data(21, new, cached, hq, hkv, d, page, dtype)
+    (wq, wq64), (wk, wk64) = weights(c["rng"], d, dtype), weights(c["rng"], d, dtype)
+    if not normed:
+        wq = wk = wq64 = wk64 = None
+    kc, vc, q = dev(c["kc"], dtype), dev(c["vc"], dtype), dev(c["q"], dtype)
+    q_out = torch.full_like(q, 9.0)
+    seqlens = dev_i32(cached)
+    libattn.device_error()
+    libattn.kvcache_append(dev(c["k"], dtype), dev(c["v"], dtype), kc, vc, dev_i32(c["cu"]), seqlens,
+                           block_table=dev_i32(c["table"]), q=q, q_out=q_out, phases=phases(rot),
+                           interleaved=inter, q_weight=wq, k_weight=wk, eps=1e-5)
+    torch.cuda.synchronize()
+    assert libattn.device_error() == (0, 0)
+    assert (seqlens.cpu().numpy() == cached).all()
+    n = sum(new)
+    _, pos = serving.token_positions(c["cu"], cached)
+    want = serving.norm_rope(f64(c["q"], dtype)[:n], pos, freqs(rot), wq64, 1e-5, inter)
+    big = np.abs(serving.norm(f64(c["q"], dtype)[:n], wq64, 1e-5)).max(-1, keepdims=True)
+    check(host(q_out)[:n], want, HALF[dtype] * np.abs(want) + 64 * U * big + TINY, "q")
+    assert (q_out[n:] == 9.0).all(), "padding rows must stay as they were"
+    rk, rv = serving.append(f64(c["k"], dtype), f64(c["v"], dtype), f64(c["kc"], dtype),
+                            f64(c["vc"], dtype), c["cu"], cached, c["table"], inv_freq=freqs(rot),
+                            weight=wk64, eps=1e-5, interleaved=inter)
+    np.testing.assert_array_equal(host(vc), rv)
+    fresh = rk != f64(c["kc"], dtype)
+    got = host(kc)
+    np.testing.assert_array_equal(got[~fresh], rk[~fresh])
+    top = np.abs(serving.norm(f64(c["k"], dtype)[:n], wk64, 1e-5)).max()
+    check(got, rk, HALF[dtype] * np.abs(rk) + np.where(fresh, 64 * U * top, 0) + TINY, "k cache")
+
+
+def test_append_without_queries_strided_and_contiguous_cache():
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    dtype, hkv, d, cap = syn.BF16, 2, 64, 40
+    rng = np.random.default_rng(22)
+    kv = dev(syn.normal_bits(rng, (11, 2, hkv, d), dtype), dtype)     # packed (T, 2, hkv, d)
+    pools = dev(syn.normal_bits(rng, (3, 2, cap, hkv, d), dtype), dtype)  # K and V pages interleaved
+    before = pools.clone()
+    new, cached = [4, 0, 7], [10, 3, 33]
+    cu = dev_i32(np.cumsum([0] + new))
+    r = libattn.kvcache_append(kv[:, 0], kv[:, 1], pools[:, 0], pools[:, 1], cu, dev_i32(cached))
+    torch.cuda.synchronize()
+    assert r is None
+    want = before.clone()
+    at = 0
+    for i, (n, c) in enumerate(zip(new, cached)):
+        want[i, :, c:c + n] = kv[at:at + n].transpose(0, 1)
+        at += n
+    assert torch.equal(pools, want)
+
+
+def test_append_bad_pages_and_lengths():
+    """A page outside the pool, a position past the table and a negative length:
+    flagged, nothing written for them, everything else as it should be."""
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    dtype, hkv, d, page = syn.F16, 1, 64, 16
+    new, cached = [2, 2, 2, 2], [0, 16, 31, 4]
+    c = append_data(23, new, cached, 2, hkv, d, page, dtype, pad=0)
+    good = libattn_append(c, dtype, cached)
+    for bit, table, seqlens, skip in (
+            (1, _with(c["table"], (1, 1), 99), cached, {2, 3}),
+            (1, _with(c["table"], (1, 1), -1), cached, {2, 3}),
+            (2, c["table"][:, :2], cached, {5}),
+            (16, c["table"], [0, -3, 31, 4], {2, 3})):
+        libattn.device_error()
+        kc, vc, _ = libattn_append(c, dtype, seqlens, table)
+        st, word = libattn.device_error()
+        assert st == 6 and word == bit, (st, word)
+        seq, pos = serving.token_positions(c["cu"], cached)
+        before = dev(c["vc"], dtype)
+        for r, (i, p) in enumerate(zip(seq, pos)):
+            pg, sl = c["table"][i, p // page], p % page
+            ref = before if r in skip else good[1]
+            assert torch.equal(vc[pg, sl], ref[pg, sl]), (bit, r)
+
+
+def _with(table, at, value):
+    t = table.copy()
+    t[at] = value
+    return t
+
+
+def libattn_append(c, dtype, seqlens, table=None):
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    kc, vc = dev(c["kc"], dtype), dev(c["vc"], dtype)
+    q_out = libattn.kvcache_append(dev(c["k"], dtype), dev(c["v"], dtype), kc, vc, dev_i32(c["cu"]),
+                                   dev_i32(seqlens), phases=phases(64), q=dev(c["q"], dtype),
+                                   block_table=dev_i32(c["table"] if table is None else table))
+    torch.cuda.synchronize()
+    return kc, vc, q_out
