@@ -146,7 +146,7 @@ int resolve_splits(int b, int hkv, int max_seqlen_k, int num_splits, int sms) {
 // Page strides in elements; 0 means contiguous pages.  A given stride must
 // hold a whole page and keep 16-byte alignment (TMA).
 bool page_stride_ok(int64_t ps, int64_t page_elems) {
-  return ps == 0 || (ps >= page_elems && ps % 8 == 0 && ps <= (int64_t)1 << 40);
+  return ps == 0 || (ps >= page_elems && ps % 8 == 0 && ps < (int64_t)1 << 38);
 }
 
 // The cache of attn_fwd_paged and attn_kvcache_append: its sizes and table.
@@ -516,8 +516,10 @@ attn_status attn_fwd_fp8(const void *q, const void *k, const void *v, void *out,
 
 size_t attn_fwd_paged_workspace_size(int batch, int total_q, int hq, int hkv, int d,
                                      int num_splits) {
-  (void)batch; (void)total_q; (void)hq; (void)hkv; (void)d; (void)num_splits;
-  return 0;
+  if (batch <= 0 || total_q <= 0 || hkv <= 0 || hq < hkv || hq % hkv || d <= 0 || num_splits < 0)
+    return 0;
+  const DeviceInfo *di = device_info();
+  return paged_plan(batch, total_q, hq, hkv, d, num_splits, di ? di->sms : 152).ws_bytes;
 }
 
 attn_status attn_fwd_paged(const void *q, const void *k_cache, const void *v_cache, void *out,
@@ -542,9 +544,12 @@ attn_status attn_fwd_paged(const void *q, const void *k_cache, const void *v_cac
   for (const void *p : {q, k_cache, v_cache, (const void *)out, (const void *)workspace})
     if (!aligned16(p)) return ATTN_ERR_INVALID;
   if ((int64_t)total_q * hq > INT32_MAX || hq > 65535) return ATTN_ERR_UNSUPPORTED;
-  const size_t need = attn_fwd_paged_workspace_size(batch, total_q, hq, hkv, d, num_splits);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
   const DeviceInfo *di = device_info();
+  const PagedPlan plan =
+      paged_plan(batch, total_q, hq, hkv, d, num_splits, di ? di->sms : 152);
+  if (plan.items > INT32_MAX || plan.slots > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
+  if (plan.ws_bytes > 0 && (!workspace || workspace_bytes < plan.ws_bytes))
+    return ATTN_ERR_WORKSPACE;
   if (!di) return ATTN_ERR_CUDA;
   const int64_t page_elems = (int64_t)page_size * hkv * d;
   PagedArgs a{};
@@ -576,7 +581,15 @@ attn_status attn_fwd_paged(const void *q, const void *k_cache, const void *v_cac
   a.err = di->err;
   a.wait_ns = wait_limit_ns();
   a.stall = test_stall();
-  return launched(launch_paged_simt(a, stream));
+  a.pack = plan.pack;
+  a.num_splits = plan.num_splits;
+  a.target = plan.target;
+  a.slots = (int)plan.slots;
+  a.o_part = static_cast<float *>(workspace);
+  a.lse_part = a.o_part + plan.slots * 128 * plan.layout * d;
+  if (num_pages == 0 || (block_table && page_size % 16 != 0))
+    return launched(launch_paged_simt(a, stream));
+  return launched(launch_paged_tc(a, plan, stream));
 }
 
 uint64_t attn_rope_phase(double inv_freq) {

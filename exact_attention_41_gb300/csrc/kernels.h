@@ -88,7 +88,26 @@ struct PagedArgs {
   int *err;
   uint64_t wait_ns;             // wall-clock limit of a device-side wait (ns)
   int stall;                    // test hook, as FwdArgs::stall
+  // work split (paged_plan): num_splits 0 cuts the keys into about `target`
+  // pieces of equal length over the whole call, 1 does not cut, n > 1 cuts
+  // every row's keys into n pieces.  Pieces of cut rows write their partial
+  // results to one of `slots` slots of the workspace.
+  int pack;                     // query heads that share a tile: g or 1
+  int num_splits, target, slots;
+  float *o_part;                // (slots, rows of a block, d)
+  float *lse_part;              // (slots, rows of a block), log2 units
 };
+
+// How attn_fwd_paged cuts its work; host only, from the sizes of the call.
+struct PagedPlan {
+  int layout;                   // query tiles of 128 rows per block
+  int pack;
+  int tile_pos;                 // query positions of one 128-row tile
+  int num_splits, target;
+  int64_t items, slots;         // blocks of the grid; partial results
+  size_t ws_bytes;
+};
+PagedPlan paged_plan(int batch, int total_q, int hq, int hkv, int d, int num_splits, int sms);
 
 // Per-head norm and rotation (attn_qk_norm_rope, its backward, and
 // attn_kvcache_append).  *_rs: elements between consecutive token rows; for
@@ -186,6 +205,8 @@ cudaError_t launch_widen_e4m3(const void *src, void *dst, int64_t n, int sms, cu
 // Debug probability matrix p (b, hq, sq, sk) fp32 from q, k and a.lse.
 cudaError_t launch_probs(const FwdArgs &a, float *p, cudaStream_t st);
 cudaError_t launch_paged_simt(const PagedArgs &a, cudaStream_t st);
+// Tensor-core form; the caches must be contiguous or page_size % 16 == 0.
+cudaError_t launch_paged_tc(const PagedArgs &a, const PagedPlan &plan, cudaStream_t st);
 // Forward of the norm and rotation, or the append when a.cu_seqlens is set.
 cudaError_t launch_norm_rope(const RopeArgs &a, int sms, cudaStream_t st);
 cudaError_t launch_norm_rope_bwd(const RopeArgs &a, int sms, cudaStream_t st);

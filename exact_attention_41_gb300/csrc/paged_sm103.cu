@@ -1,0 +1,850 @@
+// Attention of a ragged chunk of new tokens over a paged cache on the
+// 5th-generation tensor cores (sm_103a).
+//
+// The mathematics is that of the dense forward: S = Q K^T, scale, softcap,
+// mask, a running maximum and sum per query row, O += P V, one pass over the
+// keys with S and P in TMEM only.  What differs is where work and keys come
+// from.
+//
+// Work.  A block takes one item: a tile of query rows (one or two times 128;
+// with GQA the g heads of a KV head share a tile, 128 / g positions of each),
+// one KV head, and one piece of the tile's visible keys.  Lengths are known on
+// the device only, so every block finds its item itself: one warp runs over
+// cu_seqlens and cache_seqlens, 32 sequences at a time, counts each one's
+// tiles and pieces and stops where its block index falls.  The grid is the
+// largest number of items that the sizes on the host allow; blocks behind the
+// last item leave at once.  A batch of one long chunk among many single
+// tokens therefore costs no grid of longest-length rows.
+//
+// Pieces.  With few query rows the keys are cut so that the call fills the
+// GPU: all sequences' key steps together, divided by the wanted number of
+// items, give the length of a piece.  Pieces of a cut row write a normalised
+// fp32 O and its log2-sum; paged_combine_kernel joins them in piece order.
+//
+// Keys.  A K or V tile of BN keys is one TMA box where a page holds a multiple
+// of BN keys, and otherwise one box per gcd(page_size, BN) keys, issued by as
+// many lanes, each of which looks its page up one step ahead.  Boxes without a
+// visible key are not loaded and their table entries not read.  Slots outside
+// the block's visible keys may hold anything, and 0 * NaN would reach O, so the
+// producer warp zeroes those rows of the first and last V tile in shared
+// memory before their product is issued; in K they only reach scores that the
+// mask overwrites.
+//
+// Roles as in the dense forward: warp 0 producer, warp 1 MMA issuer, one
+// softmax warpgroup per 128-row tile.  Softmax warps whose 32 rows are all
+// beyond the sequence do nothing.
+#include <algorithm>
+#include <numeric>
+
+#include "paged.cuh"
+#include "sm103.cuh"
+
+namespace attn {
+namespace {
+using namespace sm103;
+
+constexpr int kBM = 128;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O when max grows > 256x
+constexpr int kMinPieceSteps = 4;          // shortest piece worth a block and a partial result
+
+// NT query tiles per block, BN keys per step, as FwdCfg in the dense forward.
+template <int D, int BN, int NT>
+struct PagedCfg {
+  static constexpr int kStages = (D == 64) ? 3 : 2;
+  static constexpr int kQBytes = kBM * D * 2;
+  static constexpr int kKVBytes = BN * D * 2;
+  static constexpr int kCols = D / 64;  // 128-byte column blocks
+  static constexpr int kSmemData = NT * kQBytes + 2 * kStages * kKVBytes;
+  static constexpr int kCtas = (NT == 1 && D <= 128) ? 2 : 1;
+  static constexpr int kSmem =
+      kCtas == 2 ? kSmemData + 1024
+                 : (kSmemData + 1024 > 120 * 1024 ? kSmemData + 1024 : 120 * 1024);
+  static constexpr int kSCol0 = NT * D;
+  static constexpr uint32_t kTmemCols = kCtas == 2 ? 256 : 512;
+  static constexpr int kThreads = NT == 2 ? 384 : 192;
+  static constexpr int kSoftmaxWarp0 = NT == 2 ? 4 : 2;
+  static_assert(NT * D + 2 * BN <= (int)kTmemCols, "TMEM budget");
+  static_assert(kCtas == 1 || 2 * (kSmem + 1024) <= 227 * 1024, "shared memory of two blocks");
+};
+
+// One unit of work.
+struct Item {
+  int seq, m0, head, piece, pieces, slot;  // m0: first query position
+  PagedSeq s;
+};
+
+// Key steps [n_lo, n_lo + nt) that query positions [m0, m0 + n) see, and the
+// first and one-past-last visible key.
+struct Steps {
+  int n_lo, nt, kb, ke;
+};
+__device__ __forceinline__ Steps key_steps(const PagedArgs &a, const PagedSeq &s, int m0, int n,
+                                           int bn) {
+  Steps r{0, 0, 0, 0};
+  const int last = min(m0 + n, s.lq) - 1;
+  if (m0 > last) return r;
+  int lo_f, hi_f, lo_l, hi_l;
+  key_range(m0, s.lq, s.lk, a.win_l, a.win_r, lo_f, hi_f);
+  key_range(last, s.lq, s.lk, a.win_l, a.win_r, lo_l, hi_l);
+  // (the ends of a row's range never decrease down the rows)
+  if (hi_l < lo_f || hi_l < 0) return r;
+  r.kb = lo_f;
+  r.ke = hi_l + 1;
+  r.n_lo = lo_f / bn;
+  r.nt = hi_l / bn - r.n_lo + 1;
+  return r;
+}
+
+__device__ __forceinline__ int64_t warp_sum64(int64_t x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Item `idx` of the call; false behind the last one.  Whole warp; `pos` query
+// positions per block.  raise: report bad lengths (one block of the grid does).
+__device__ __forceinline__ bool find_item(const PagedArgs &a, int64_t idx, int pos, int bn,
+                                          bool raise, Item &it) {
+  const int lane = threadIdx.x & 31;
+  const int nh = a.pack > 1 ? a.hkv : a.hq;
+  // tiles and longest key range of sequence i
+  auto shape = [&](int i, PagedSeq &s, int &mt, int &steps) {
+    mt = steps = 0;
+    if (i >= a.batch) return;
+    s = paged_seq(a, i);
+    mt = (s.lq + pos - 1) / pos;
+    if (mt == 0) return;
+    steps = max(key_steps(a, s, 0, pos, bn).nt, key_steps(a, s, (mt - 1) * pos, pos, bn).nt);
+  };
+  int64_t piece_steps = INT64_MAX;
+  if (a.num_splits == 0) {
+    int64_t work = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      PagedSeq s;
+      int mt, steps;
+      shape(b0 + lane, s, mt, steps);
+      work += (int64_t)mt * steps;
+    }
+    work = warp_sum64(work) * nh;
+    piece_steps = max((int64_t)kMinPieceSteps, (work + a.target - 1) / a.target);
+  }
+  int64_t base = 0, slots = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    PagedSeq s{0, 0, 0, 0};
+    int mt, steps;
+    shape(b0 + lane, s, mt, steps);
+    if (raise && s.err) raise_error(a.err, s.err);
+    int pieces = 1;
+    if (a.num_splits == 0)
+      pieces = max(1, (int)((steps + piece_steps - 1) / piece_steps));
+    else
+      pieces = max(1, min(a.num_splits, steps));
+    const int64_t n = (int64_t)mt * pieces * nh;
+    int64_t incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, idx < base + incl);
+    const int64_t cut = pieces > 1 ? n : 0;
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      slots += warp_sum64(lane < src ? cut : 0);
+      const int local = (int)(idx - base - __shfl_sync(0xffffffffu, incl - n, src));
+      it.seq = b0 + src;
+      it.pieces = __shfl_sync(0xffffffffu, pieces, src);
+      const int tiles = __shfl_sync(0xffffffffu, mt, src);
+      it.s.q0 = __shfl_sync(0xffffffffu, s.q0, src);
+      it.s.lq = __shfl_sync(0xffffffffu, s.lq, src);
+      it.s.lk = __shfl_sync(0xffffffffu, s.lk, src);
+      it.s.err = 0;
+      // heads fastest (they share a sequence's pages and, in L2, its K and V),
+      // then pieces; the last positions, which see the most keys, first
+      it.head = local % nh;
+      it.piece = local / nh % it.pieces;
+      it.m0 = (tiles - 1 - local / nh / it.pieces) * pos;
+      it.slot = it.pieces > 1 ? (int)(slots + local) : -1;
+      return true;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+    slots += warp_sum64(cut);
+  }
+  return false;
+}
+
+struct Shared {
+  uint64_t q_full;
+  uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3];
+  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t v_clean[2];  // first / last V tile: rows that no query sees are zeroed
+  uint64_t all_done;    // every MMA of the block has completed
+  uint64_t wait_ns;
+  Item item;
+  uint32_t tmem_base;
+  int live, abort;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ bool wait_bar(Shared &sh, uint64_t *bar, uint32_t parity, int *err) {
+  return mbar_wait_bounded(smem_u32(bar), parity, &sh.abort, err, sh.wait_ns);
+}
+// The same wait taken by a whole warp with one answer.
+__device__ __forceinline__ bool wait_warp(Shared &sh, uint64_t *bar, uint32_t parity, int *err) {
+  return __all_sync(0xffffffffu, wait_bar(sh, bar, parity, err));
+}
+
+template <typename T> struct IsBf16 { static constexpr int v = 0; };
+template <> struct IsBf16<__nv_bfloat16> { static constexpr int v = 1; };
+
+template <typename T, int D, int BN, int NT>
+__global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN, NT>::kCtas)
+    paged_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                    const __grid_constant__ CUtensorMap tv, const PagedArgs a, const int tile_pos,
+                    const int box_rows) {
+  using C = PagedCfg<D, BN, NT>;
+  constexpr int ST = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared sh;
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~uintptr_t(1023));
+  uint8_t *q_s = smem;
+  uint8_t *k_s = smem + NT * C::kQBytes;
+  uint8_t *v_s = k_s + ST * C::kKVBytes;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pg = a.pack;
+  if (warp == 0) {
+    Item it{};
+    it.pieces = 1;
+    const bool live = find_item(a, blockIdx.x, tile_pos * NT, BN, blockIdx.x == 0, it);
+    if (lane == 0) {
+      sh.item = it;
+      sh.live = live;
+      mbar_init(&sh.q_full, 1);
+      for (int s = 0; s < ST; ++s) {
+        mbar_init(&sh.k_full[s], 1);
+        mbar_init(&sh.k_empty[s], 1);
+        mbar_init(&sh.v_full[s], 1);
+        mbar_init(&sh.v_empty[s], 1);
+      }
+      // softmax threads that take part: warps with a row of the sequence
+      for (int s = 0; s < 2; ++s) {
+        const int t = NT == 2 ? s : 0;
+        const int rows = min(max(it.s.lq - it.m0 - t * tile_pos, 0), tile_pos) * pg;
+        mbar_init(&sh.s_full[s], 1);
+        mbar_init(&sh.p_full[s], max(1, (rows + 31) / 32 * 32));
+        mbar_init(&sh.o_done[s], 1);
+        mbar_init(&sh.v_clean[s], 1);
+      }
+      mbar_init(&sh.all_done, 1);
+      sh.wait_ns = a.wait_ns;
+      sh.abort = 0;
+      fence_mbar_init();
+    }
+  } else if (warp == 1) {
+    tmem_alloc(&sh.tmem_base, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;
+  const Item it = sh.item;
+  const PagedSeq sq = it.s;
+  const int kvh = pg > 1 ? it.head : it.head / (a.hq / a.hkv);
+  const int h = pg > 1 ? kvh * pg : it.head;  // (first) query head of the rows
+
+  // The block's key steps, and this piece of them.
+  const Steps all = key_steps(a, sq, it.m0, tile_pos * NT, BN);
+  const int per = (all.nt + it.pieces - 1) / it.pieces;
+  const int p_lo = min(it.piece * per, all.nt);
+  // behind the last item, or a piece behind the last key (the combine step
+  // skips it by the same test): nothing to do
+  const bool live = sh.live && (it.piece == 0 || p_lo < all.nt);
+  const int n_lo = all.n_lo + p_lo;                             // first step of the piece
+  const int nt = live ? min(all.nt - p_lo, per) : 0;            // and how many
+  // steps [ta, tb) of the piece that tile t takes part in: those with a key
+  // that one of its rows sees
+  auto tile_steps = [&](int t, int &ta, int &tb) {
+    const Steps x = key_steps(a, sq, it.m0 + t * tile_pos, tile_pos, BN);
+    ta = min(max(x.n_lo - n_lo, 0), nt);
+    tb = min(max(x.n_lo + x.nt - n_lo, ta), nt);
+    if (x.nt == 0) ta = tb = 0;
+  };
+  // V rows of the piece's first and last step that lie outside [kb, ke)
+  const int front = nt > 0 ? max(0, all.kb - n_lo * BN) : 0;
+  const int back = nt > 0 ? max(0, (n_lo + nt) * BN - all.ke) : 0;
+
+  if (warp < C::kSoftmaxWarp0) {
+    if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      if (nt > 0) {
+        const int boxes = BN / box_rows;
+        const int box = lane / C::kCols, col = lane % C::kCols;
+        // this lane's box of step j: page (-1: not needed, -2: outside the
+        // pool) and slot
+        auto locate = [&](int j, int &page, int &slot) {
+          const int row0 = (n_lo + j) * BN + box * box_rows;
+          page = -1;
+          slot = 0;
+          if (box < boxes && j < nt && row0 < all.ke && row0 + box_rows > all.kb) {
+            const int lp = a.block_table ? row0 / a.page_size : 0;
+            slot = row0 - lp * a.page_size;
+            page = paged_page(a, it.seq, lp);
+            if (page < 0) page = -2;
+          }
+        };
+        int page, slot;
+        locate(0, page, slot);
+        if (lane == 0) {
+          prefetch_tmap(&tq);
+          prefetch_tmap(&tk);
+          prefetch_tmap(&tv);
+          const int q_rows = tile_pos * pg;
+          mbar_expect_tx(&sh.q_full, NT * q_rows * D * 2);
+          for (int t = 0; t < NT; ++t)
+            for (int c = 0; c < C::kCols; ++c)
+              tma_load_3d(q_s + t * C::kQBytes + c * kBM * 128, &tq, &sh.q_full, c * 64, h,
+                          sq.q0 + it.m0 + t * tile_pos);
+        }
+        // zeroes rows [r0, r1) of V tile j once it has landed
+        auto clean = [&](int j, int r0, int r1, uint64_t *bar) {
+          if (!wait_warp(sh, &sh.v_full[j % ST], (j / ST) & 1, a.err)) return;
+          uint8_t *tile = v_s + (j % ST) * C::kKVBytes;
+          for (int x = lane; x < (r1 - r0) * C::kCols * 8; x += 32) {
+            const int row = r0 + x / 8 % (r1 - r0), c = x / 8 / (r1 - r0);
+            *reinterpret_cast<uint4 *>(tile + c * (BN * 128) + row * 128 + x % 8 * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar);
+        };
+        const int front_after = min(ST, nt) - 1;  // step after whose loads the first tile is cleaned
+        int issued = 0;                            // K and V loads: 2 per step
+        for (int j = 0; j < nt; ++j) {
+          const int st = j % ST;
+          const uint32_t ph = ((j / ST) & 1) ^ 1;
+          if (__any_sync(0xffffffffu, page == -2)) {
+            if (lane == 0) {
+              raise_error(a.err, kErrPageOutOfRange);
+              *(volatile int *)&sh.abort = 1;
+            }
+            break;
+          }
+          const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, page >= 0)) * box_rows * 128;
+          const int pnow = page, snow = slot;
+          locate(j + 1, page, slot);
+          const int dst = st * C::kKVBytes + col * (BN * 128) + box * box_rows * 128;
+          if (!wait_warp(sh, &sh.k_empty[st], ph, a.err)) break;
+          if (lane == 0) mbar_expect_tx(&sh.k_full[st], bytes);
+          __syncwarp();
+          if (pnow >= 0) tma_load_4d(k_s + dst, &tk, &sh.k_full[st], col * 64, kvh, snow, pnow);
+          issued = 2 * j + 1;
+          if (!wait_warp(sh, &sh.v_empty[st], ph, a.err)) break;
+          if (lane == 0) mbar_expect_tx(&sh.v_full[st], bytes);
+          __syncwarp();
+          if (pnow >= 0) tma_load_4d(v_s + dst, &tv, &sh.v_full[st], col * 64, kvh, snow, pnow);
+          issued = 2 * j + 2;
+          if (j == front_after && front > 0) clean(0, 0, min(front, BN), &sh.v_clean[0]);
+        }
+        if (issued == 2 * nt && back > 0) clean(nt - 1, BN - back, BN, &sh.v_clean[1]);
+        __syncwarp();
+        if (*(volatile int *)&sh.abort) {
+          // let this block's copies in flight land before it exits
+          int *noerr = nullptr;
+          mbar_wait(&sh.q_full, 0, noerr);
+          for (int x = max(0, issued - 2 * ST); x < issued; ++x) {
+            const int j = x / 2, st = j % ST;
+            mbar_wait(x % 2 ? &sh.v_full[st] : &sh.k_full[st], (j / ST) & 1, noerr);
+          }
+        }
+      }
+    } else if (warp == 1) {
+      // -------------------------------------------------------- MMA issuer
+      if (elect_one() && live) {
+        constexpr int ab = IsBf16<T>::v;
+        constexpr uint32_t id_s = idesc_f16(kBM, BN, ab, 0, 0);
+        constexpr uint32_t id_o = idesc_f16(kBM, D, ab, 0, 1);
+        const uint64_t q_d = smem_desc(smem_u32(q_s), 16, 1024);
+        const uint64_t k_d = smem_desc(smem_u32(k_s), 16, 1024);
+        const uint64_t v_d = smem_desc(smem_u32(v_s), BN * 128, 1024);
+        auto mma_s = [&](int t, int j, uint32_t dcol) {
+          const uint32_t ko = (j % ST) * C::kKVBytes;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t ad =
+                desc_add(q_d, t * C::kQBytes + (kk / 4) * (kBM * 128) + (kk % 4) * 32);
+            const uint64_t bd = desc_add(k_d, ko + (kk / 4) * (BN * 128) + (kk % 4) * 32);
+            mma_ss(dcol, ad, bd, id_s, kk > 0);
+          }
+        };
+        auto mma_pv = [&](int t, int j, uint32_t pcol, bool first) {
+          const uint32_t vo = (j % ST) * C::kKVBytes;
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk) {
+            const uint64_t bd = desc_add(v_d, vo + kk * 16 * 128);
+            mma_ts(tmem + t * D, pcol + kk * 8, bd, id_o, (!first || kk > 0) ? 1u : 0u);
+          }
+        };
+        auto k_ready = [&](int j) {
+          const bool r = wait_bar(sh, &sh.k_full[j % ST], (j / ST) & 1, a.err);
+          tc_fence_after();
+          return r;
+        };
+        auto v_ready = [&](int j) {
+          bool r = wait_bar(sh, &sh.v_full[j % ST], (j / ST) & 1, a.err);
+          if (r && j == 0 && front > 0) r = wait_bar(sh, &sh.v_clean[0], 0, a.err);
+          if (r && j == nt - 1 && back > 0) r = wait_bar(sh, &sh.v_clean[1], 0, a.err);
+          tc_fence_after();
+          return r;
+        };
+        int ta[NT], tb[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) tile_steps(t, ta[t], tb[t]);
+        // test hook: all_done completes only after this thread's last commit
+        const bool stalled = a.stall && !wait_bar(sh, &sh.all_done, 0, a.err);
+        if (stalled) {
+        } else if (NT == 2) {
+          // S_0(0) S_1(0) | PV_0(j) S_0(j+1) PV_1(j) S_1(j+1) | ..., where a
+          // tile takes part in step j only inside its own range; every K and V
+          // tile is waited for once before its stage is released
+          bool ok = nt == 0 || (wait_bar(sh, &sh.q_full, 0, a.err) && k_ready(0));
+          if (ok && nt > 0) {
+            for (int t = 0; t < NT; ++t) {
+              if (ta[t] == 0 && tb[t] > 0) {
+                mma_s(t, 0, tmem + C::kSCol0 + t * BN);
+                mma_commit(&sh.s_full[t]);
+              }
+            }
+            mma_commit(&sh.k_empty[0]);
+          }
+          for (int j = 0; ok && j < nt; ++j) {
+            const bool k_next = j + 1 < nt;
+            const int last_pv = (j >= ta[1] && j < tb[1]) ? 1 : 0;
+            const int last_s = (j + 1 >= ta[1] && j + 1 < tb[1]) ? 1 : 0;
+            bool v_in = false, k_in = false;
+            for (int t = 0; t < NT && ok; ++t) {
+              const uint32_t scol = tmem + C::kSCol0 + t * BN;
+              if (j >= ta[t] && j < tb[t]) {
+                if (!wait_bar(sh, &sh.p_full[t], (j - ta[t]) & 1, a.err)) { ok = false; break; }
+                tc_fence_after();
+                if (!v_in && !(v_in = v_ready(j))) { ok = false; break; }
+                mma_pv(t, j, scol, j == ta[t]);
+                mma_commit(&sh.o_done[t]);
+                if (t == last_pv) mma_commit(&sh.v_empty[j % ST]);
+              }
+              if (k_next && j + 1 >= ta[t] && j + 1 < tb[t]) {
+                if (!k_in && !(k_in = k_ready(j + 1))) { ok = false; break; }
+                mma_s(t, j + 1, scol);
+                mma_commit(&sh.s_full[t]);
+                if (t == last_s) mma_commit(&sh.k_empty[(j + 1) % ST]);
+              }
+            }
+            if (ok && !v_in) {
+              if (!v_ready(j)) break;
+              mma_commit(&sh.v_empty[j % ST]);
+            }
+            if (ok && k_next && !k_in) {
+              if (!k_ready(j + 1)) break;
+              mma_commit(&sh.k_empty[(j + 1) % ST]);
+            }
+          }
+        } else {
+          bool ok = nt == 0 || (wait_bar(sh, &sh.q_full, 0, a.err) && k_ready(0));
+          if (ok && nt > 0) {
+            mma_s(0, 0, tmem + C::kSCol0);
+            mma_commit(&sh.s_full[0]);
+            mma_commit(&sh.k_empty[0]);
+          }
+          for (int j = 0; ok && j < nt; ++j) {
+            if (j + 1 < nt) {
+              if (!k_ready(j + 1)) break;
+              mma_s(0, j + 1, tmem + C::kSCol0 + ((j + 1) & 1) * BN);
+              mma_commit(&sh.s_full[(j + 1) & 1]);
+              mma_commit(&sh.k_empty[(j + 1) % ST]);
+            }
+            if (!wait_bar(sh, &sh.p_full[j & 1], (j >> 1) & 1, a.err)) break;
+            tc_fence_after();
+            if (!v_ready(j)) break;
+            mma_pv(0, j, tmem + C::kSCol0 + (j & 1) * BN, j == 0);
+            mma_commit(&sh.o_done[0]);
+            mma_commit(&sh.v_empty[j % ST]);
+          }
+        }
+        // after an abort, no MMA may still run when the TMEM is released
+        mma_commit(&sh.all_done);
+        if (*(volatile int *)&sh.abort) {
+          int *noerr = nullptr;
+          mbar_wait(&sh.all_done, 0, noerr);
+        }
+      }
+    }
+  } else {
+    if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
+    // ------------------------------------------------------------ softmax
+    const int t = (warp - C::kSoftmaxWarp0) >> 2;  // query tile of this warpgroup
+    const int r0 = 32 * (warp & 3), r = r0 + lane;  // TMEM lane = row in the tile
+    const int first = it.m0 + t * tile_pos;         // the tile's first query position
+    const int rows = min(max(sq.lq - first, 0), tile_pos) * pg;  // its rows in the sequence
+    if (live && r0 < rows) {
+      const int i = first + r / pg;  // query position
+      const int hr = h + r % pg;     // and query head
+      const uint32_t lane_off = (uint32_t)r0 << 16;
+      const uint32_t o_t = tmem + lane_off + t * D;
+      int lo_i, hi_i;
+      key_range(i, sq.lq, sq.lk, a.win_l, a.win_r, lo_i, hi_i);
+      const uint32_t n_vis = (uint32_t)max(hi_i - lo_i + 1, 0);  // keys this row sees
+      // steps that need no mask: every row of the tile sees every key of them
+      int lo_tile_max, hi_tile_min, dummy;
+      key_range(min(first + tile_pos, sq.lq) - 1, sq.lq, sq.lk, a.win_l, a.win_r, lo_tile_max, dummy);
+      key_range(first, sq.lq, sq.lk, a.win_l, a.win_r, dummy, hi_tile_min);
+      // not 0: a masked -inf times the scale has to stay -inf (scores of a
+      // scale this small are 0 beside the 1 in every exponential)
+      const float sl2 = fmaxf(a.scale * kLog2e, 1e-30f);
+      const bool cap = a.softcap > 0.f;
+      const float cap_in = cap ? a.scale / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
+      const float cap_k = cap_in * 2.8853900817779268f;  // 2 log2(e) cap_in
+      float m_ref = -INFINITY, l = 0.f;
+      bool ok = true;
+      int ta, tb;
+      tile_steps(t, ta, tb);
+      const int ntt = tb - ta;
+      for (int j = 0; j < ntt; ++j) {
+        const int key0 = (n_lo + ta + j) * BN;
+        const int sb = NT == 2 ? t : (j & 1);  // S/P buffer and its barriers
+        const uint32_t s_par = NT == 2 ? (j & 1) : ((j >> 1) & 1);
+        if (!wait_warp(sh, &sh.s_full[sb], s_par, a.err)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t scol = tmem + lane_off + C::kSCol0 + sb * BN;
+        float x[BN];
+        {
+          uint32_t u[BN];
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c)
+            tmem_ld32(scol + c * 32, *reinterpret_cast<uint32_t(*)[32]>(u + c * 32));
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < BN; ++e) x[e] = __uint_as_float(u[e]);
+        }
+        // softcap, then the mask
+        if (cap) {
+          // c tanh(x cap_in) in log2 units = cap_out - 2 cap_out / (e^{2 x cap_in} + 1)
+          const uint64_t k2 = f2_pack(cap_k, cap_k), one2 = f2_pack(1.f, 1.f);
+          const uint64_t co2 = f2_pack(cap_out, cap_out);
+          const uint64_t mco2 = f2_pack(-2.f * cap_out, -2.f * cap_out);
+#pragma unroll
+          for (int e = 0; e < BN; e += 2) {
+            float a0, a1, y0, y1;
+            f2_unpack(f2_mul(f2_pack(x[e], x[e + 1]), k2), a0, a1);
+            f2_unpack(f2_add(f2_pack(ex2(a0), ex2(a1)), one2), y0, y1);
+            f2_unpack(f2_fma(f2_pack(rcp_approx(y0), rcp_approx(y1)), mco2, co2), x[e], x[e + 1]);
+          }
+        }
+        if (key0 < lo_tile_max || key0 + BN - 1 > hi_tile_min) {
+          // visible: e - (lo_i - key0) in [0, n_vis), one unsigned compare per key
+          const int e_lo = lo_i - key0;
+#pragma unroll
+          for (int e = 0; e < BN; ++e)
+            if ((uint32_t)(e - e_lo) >= n_vis) x[e] = -INFINITY;
+        }
+        // raw-score max: scale and softcap preserve the order (scale >= 0)
+        float mp[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) mp[u] = x[u];
+#pragma unroll
+        for (int e = 8; e + 16 <= BN; e += 16) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) mp[u] = fmax3(mp[u], x[e + u], x[e + 8 + u]);
+        }
+        if constexpr ((BN - 8) % 16 != 0) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) mp[u] = fmaxf(mp[u], x[BN - 8 + u]);
+        }
+        const float mt = fmaxf(fmax3(mp[0], mp[1], mp[2]),
+                               fmax3(fmax3(mp[3], mp[4], mp[5]), mp[6], mp[7]));
+        const float f = cap ? 1.f : sl2;  // x * f is the score in log2 units
+        const float m_new = fmaxf(m_ref, mt * f);
+        const bool rescale = m_new > m_ref + kRescaleThreshold;
+        float alpha = 1.f;
+        if (rescale) {
+          alpha = ex2(m_ref - m_new);
+          l *= alpha;
+          m_ref = m_new;
+        }
+        const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+        const uint64_t f2 = f2_pack(f, f), nm2 = f2_pack(neg_m, neg_m);
+        uint64_t rs[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) rs[u] = 0ull;
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int el = c * 32 + 2 * e;
+            float t0, t1;
+            f2_unpack(f2_fma(f2_pack(x[el], x[el + 1]), f2, nm2), t0, t1);
+            const float p0 = ex2(t0), p1 = ex2(t1);
+            rs[e & 3] = f2_add(rs[e & 3], f2_pack(p0, p1));
+            pk[e] = Elem<T>::from_f2(p0, p1);
+          }
+          tmem_st16(scol + c * 16, pk);
+        }
+        {
+          float y[8];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) f2_unpack(rs[u], y[2 * u], y[2 * u + 1]);
+          l += ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
+        }
+        tmem_wait_st();
+        if (j > 0) {
+          // O holds P_{j-1} V_{j-1} once this completes; only then may it be rescaled
+          if (!wait_warp(sh, &sh.o_done[t], (j - 1) & 1, a.err)) { ok = false; break; }
+          tc_fence_after();
+          if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t u[32];
+              tmem_ld32(o_t + c * 32, u);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+              tmem_st32(o_t + c * 32, u);
+            }
+            tmem_wait_st();
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&sh.p_full[sb]);
+      }
+      // epilogue.  all_done, not the tile's own last step: a page outside the
+      // pool anywhere in the piece then empties both tiles, every run alike.
+      ok = __all_sync(0xffffffffu, ok && wait_bar(sh, &sh.all_done, 0, a.err) &&
+                                       !*(volatile int *)&sh.abort);
+      tc_fence_after();
+      if (!ok) l = 0.f;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float lse2 = l > 0.f ? (m_ref == -INFINITY ? 0.f : m_ref) + __log2f(l) : -INFINITY;
+      const bool valid = r < rows;
+      T *orow = static_cast<T *>(a.o) + ((int64_t)(sq.q0 + i) * a.hq + hr) * D;
+      const int64_t part = (int64_t)it.slot * (NT * kBM) + t * kBM + r;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t u[32];
+        if (ok && ntt > 0) {
+          tmem_ld32(o_t + c * 32, u);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) u[e] = 0u;
+        }
+        if (it.pieces == 1) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            w[e] = Elem<T>::from_f2(__uint_as_float(u[2 * e]) * inv, __uint_as_float(u[2 * e + 1]) * inv);
+          if (valid) {
+            uint4 *dst = reinterpret_cast<uint4 *>(orow + c * 32);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+          }
+        } else if (valid && it.slot < a.slots) {
+          float4 *dst = reinterpret_cast<float4 *>(a.o_part + part * D + c * 32);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[e] = make_float4(__uint_as_float(u[4 * e]) * inv, __uint_as_float(u[4 * e + 1]) * inv,
+                                 __uint_as_float(u[4 * e + 2]) * inv,
+                                 __uint_as_float(u[4 * e + 3]) * inv);
+        }
+      }
+      if (valid) {
+        if (it.pieces == 1)
+          a.lse[(int64_t)hr * a.total_q + sq.q0 + i] = lse2 * kLn2;
+        else if (it.slot < a.slots)
+          a.lse_part[part] = lse2;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+}
+
+constexpr int kCombineWarps = 4;
+
+// Joins the pieces of cut rows, one warp per row: with l_p the log2-sums,
+// L = log2 sum 2^l_p and O = sum 2^(l_p - L) O_p, in piece order.  One block per
+// item and row group; the first piece's block of a tile does the work.
+template <typename T, int D, int BN, int NT>
+__global__ void __launch_bounds__(kCombineWarps * 32)
+    paged_combine_kernel(const PagedArgs a, const int tile_pos) {
+  constexpr int V = D / 32;
+  __shared__ Item item;
+  __shared__ int live;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {
+    Item it{};
+    it.pieces = 1;
+    const bool l = find_item(a, blockIdx.x, tile_pos * NT, BN, false, it);
+    if (lane == 0) {
+      item = it;
+      live = l && it.piece == 0 && it.pieces > 1;
+    }
+  }
+  __syncthreads();
+  if (!live) return;
+  const Item it = item;
+  const int pg = a.pack, nh = pg > 1 ? a.hkv : a.hq;
+  const Steps all = key_steps(a, it.s, it.m0, tile_pos * NT, BN);
+  const int per = (all.nt + it.pieces - 1) / it.pieces;
+  const int n = max(1, all.nt == 0 ? 1 : (all.nt + per - 1) / per);  // pieces that were written
+  // pieces of one tile and head are nh slots apart
+  if ((int64_t)it.slot + (int64_t)(n - 1) * nh >= a.slots) return;
+  for (int x = blockIdx.y * kCombineWarps + warp; x < NT * tile_pos * pg;
+       x += gridDim.y * kCombineWarps) {
+    const int t = x / (tile_pos * pg), r = x % (tile_pos * pg);
+    const int i = it.m0 + t * tile_pos + r / pg;
+    if (i >= it.s.lq) break;  // (rows come in order of position)
+    const int hr = pg > 1 ? it.head * pg + r % pg : it.head;
+    const int64_t step = (int64_t)nh * (NT * kBM);  // rows from a piece to the next
+    const int64_t row0 = (int64_t)it.slot * (NT * kBM) + t * kBM + r;
+    float m = -INFINITY;
+    for (int p = lane; p < n; p += 32) m = fmaxf(m, a.lse_part[row0 + p * step]);
+    m = warp_max(m);
+    float acc[V], sum = 0.f;
+#pragma unroll
+    for (int u = 0; u < V; ++u) acc[u] = 0.f;
+    if (m > -INFINITY) {
+      for (int p0 = 0; p0 < n; p0 += 32) {
+        const float w_mine =
+            p0 + lane < n ? exp2f(a.lse_part[row0 + (p0 + lane) * step] - m) : 0.f;
+        sum += warp_sum(w_mine);
+        const int k = min(32, n - p0);
+#pragma unroll 4
+        for (int p = 0; p < k; ++p) {
+          const float w = __shfl_sync(0xffffffffu, w_mine, p);
+          const float *src = a.o_part + (row0 + (p0 + p) * step) * D + lane * V;
+#pragma unroll
+          for (int u = 0; u < V; ++u) acc[u] = fmaf(w, src[u], acc[u]);
+        }
+      }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int u = 0; u < V; ++u) acc[u] *= inv;
+    store_vec<T, V>(static_cast<T *>(a.o) + ((int64_t)(it.s.q0 + i) * a.hq + hr) * D + lane * V, acc);
+    if (lane == 0)
+      a.lse[(int64_t)hr * a.total_q + it.s.q0 + i] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+  }
+}
+
+// (page, slot, head, D) pool, box {64, 1, box_rows, 1}, 128-byte swizzle.
+bool make_pool_map(CUtensorMap *m, const void *base, const PagedArgs &a, int64_t page_stride,
+                   int box_rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)a.d, (cuuint64_t)a.hkv, (cuuint64_t)a.page_size,
+                        (cuuint64_t)a.num_pages};
+  cuuint64_t strides[3] = {(cuuint64_t)a.d * 2, (cuuint64_t)a.hkv * a.d * 2,
+                           (cuuint64_t)page_stride * 2};
+  cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, a.dtype == ATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+             4, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D, int BN, int NT>
+cudaError_t paged(const PagedArgs &a, const PagedPlan &plan, cudaStream_t st) {
+  using C = PagedCfg<D, BN, NT>;
+  // a box never leaves its page
+  const int box_rows = a.block_table ? std::gcd(a.page_size, BN) : BN;
+  CUtensorMap tq, tk, tv;
+  if (!make_map_3d(&tq, a.q, a.dtype, a.total_q, a.hq, D, plan.tile_pos, a.q_rs, a.pack) ||
+      !make_pool_map(&tk, a.k_cache, a, a.k_ps, box_rows) ||
+      !make_pool_map(&tv, a.v_cache, a, a.v_ps, box_rows))
+    return cudaErrorInvalidValue;
+  cudaError_t e = set_smem_once<paged_tc_kernel<T, D, BN, NT>>(C::kSmem);
+  if (e == cudaSuccess && NT == 2)  // 128 * 88 + 256 * 208 after setmaxnreg
+    e = check_regs_once<paged_tc_kernel<T, D, BN, NT>>(C::kThreads, 128 * 88 + 256 * 208);
+  if (e != cudaSuccess) return e;
+  debug_log("paged: paged_tc_kernel d=%d, %d query tile(s) of 128 rows per block, %d-key tiles in "
+            "boxes of %d, pack=%d, num_splits=%d (target %d), grid=%lld x %d threads, smem=%d B",
+            D, NT, BN, box_rows, a.pack, a.num_splits, a.target, (long long)plan.items, C::kThreads,
+            C::kSmem);
+  paged_tc_kernel<T, D, BN, NT><<<(unsigned)plan.items, C::kThreads, C::kSmem, st>>>(
+      tq, tk, tv, a, plan.tile_pos, box_rows);
+  count_launches(1);
+  if (a.num_splits != 1) {
+    const int64_t rows = std::max<int64_t>(1, (int64_t)a.total_q * a.pack / a.batch);
+    const int groups = (int)std::min<int64_t>(NT * 8, (rows + 15) / 16);
+    paged_combine_kernel<T, D, BN, NT><<<dim3((unsigned)plan.items, groups), kCombineWarps * 32, 0, st>>>(
+        a, plan.tile_pos);
+    count_launches(1);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+PagedPlan paged_plan(int batch, int total_q, int hq, int hkv, int d, int num_splits, int sms) {
+  PagedPlan p{};
+  const int g = hq / hkv;
+  // The g query heads of a KV head share tiles: K and V are then read once for
+  // all of them.  Not where their rows fill less than three quarters of a tile
+  // (g = 44 .. 95 or above 128 leaves 128 % g rows empty) and the chunks are long
+  // enough to fill tiles of one head.
+  const int used = g <= 128 ? 128 / g * g : 0;
+  p.pack = used >= 96 || (used > 0 && total_q < 64 * (int64_t)batch) ? g : 1;
+  p.tile_pos = kBM / p.pack;
+  // two tiles per block (every K/V tile then serves 256 rows) where the
+  // average sequence fills two such blocks
+  p.layout = d == 128 && (int64_t)total_q * p.pack >= 512 * (int64_t)batch ? 2 : 1;
+  const int nh = p.pack > 1 ? hkv : hq;
+  const int pos = p.tile_pos * p.layout;
+  const int64_t wave = (int64_t)sms * (p.layout == 1 && d <= 128 ? 2 : 1);
+  // sum of ceil(n_i / pos) over sequences of sum total_q
+  const int64_t tiles = (total_q / pos + std::min(batch, total_q)) * (int64_t)nh;
+  p.num_splits = num_splits;
+  // enough tiles for several waves even if no sequence leaves one half empty
+  if (num_splits == 0 && (int64_t)(total_q + pos - 1) / pos * nh >= 4 * wave) p.num_splits = 1;
+  p.target = (int)(2 * wave);
+  if (p.num_splits == 0) {
+    // cut pieces: below 2 target (each cut tile has at least one piece of full
+    // length, and full pieces are at most target)
+    p.items = tiles + p.target;
+    p.slots = std::min<int64_t>(2 * (int64_t)p.target, p.items);
+  } else {
+    p.items = tiles * p.num_splits;
+    p.slots = p.num_splits > 1 ? p.items : 0;
+  }
+  p.ws_bytes = (size_t)p.slots * kBM * p.layout * (d + 1) * sizeof(float);
+  return p;
+}
+
+cudaError_t launch_paged_tc(const PagedArgs &a, const PagedPlan &plan, cudaStream_t st) {
+  const bool bf = a.dtype == ATTN_BF16;
+  switch (a.d) {
+    case 64:
+      return bf ? paged<__nv_bfloat16, 64, 64, 1>(a, plan, st) : paged<__half, 64, 64, 1>(a, plan, st);
+    case 128:
+      if (plan.layout == 2)
+        return bf ? paged<__nv_bfloat16, 128, 128, 2>(a, plan, st) : paged<__half, 128, 128, 2>(a, plan, st);
+      return bf ? paged<__nv_bfloat16, 128, 64, 1>(a, plan, st) : paged<__half, 128, 64, 1>(a, plan, st);
+    case 256:
+      return bf ? paged<__nv_bfloat16, 256, 64, 1>(a, plan, st) : paged<__half, 256, 64, 1>(a, plan, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace attn

@@ -266,3 +266,26 @@ def test_offsets_out_of_order_or_past_the_rows():
         st, word = libattn.device_error()
         assert st == 6 and word & 16, (cu, st, word)
         assert (out[18:] == 7.0).all() and (lse[8 * 18:] == 7.0).all()
+
+
+@pytest.mark.parametrize("d,new", [(64, 40), (128, 40), (128, 1500), (256, 40)])
+def test_wait_timeout_is_reported_and_recoverable(d, new):
+    """Every layout: the MMA issuer's first wait can only run out; the call is
+    abandoned with the timeout bit, and the next one is right."""
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    c = make(13, [new, 3], [200, 500], 8, 2, d, 32, syn.BF16)
+    libattn.device_error()
+    prev = libattn.set_wait_limit_ns(1_000_000)
+    libattn.set_test_stall(True)
+    try:
+        call(c, causal=True)
+        torch.cuda.synchronize()
+    finally:
+        libattn.set_test_stall(False)
+        libattn.set_wait_limit_ns(prev)
+    st, word = libattn.device_error()
+    assert st == 5 and word & 8, (st, word)
+    run(c, causal=True)

@@ -35,11 +35,20 @@ def paged(lib, **over):
     (dict(q_rs=4 * 128 - 8), 1), (dict(q_rs=4 * 128 + 4), 1), (dict(k_ps=64 * 2 * 128 - 8), 1),
     (dict(v_ps=64 * 2 * 128 + 4), 1), (dict(bt=None), 1), (dict(bt=None, num_pages=2), 1),
     (dict(scale=float("nan")), 1), (dict(wl=-2), 1), (dict(cap=float("nan")), 1),
-    (dict(max_pages=1 << 26), 2),
+    (dict(max_pages=1 << 26), 2), (dict(splits=8, n=0), 3), (dict(splits=8, ws=None), 3),
     (dict(batch=0), 0), (dict(total=0), 0),
 ])
 def test_paged_refusals(lib, over, status):
     assert paged(lib, **over) == status
+
+
+def test_paged_workspace_size(lib):
+    size = lib.attn_fwd_paged_workspace_size
+    assert size(4, 100, 32, 8, 128, 1) == 0          # one key range per row: no partials
+    assert size(0, 100, 32, 8, 128, 0) == 0 and size(4, 0, 32, 8, 128, 0) == 0
+    # 4 key ranges: at least the partial outputs of every row
+    assert size(4, 100, 32, 8, 128, 4) >= 4 * 100 * 32 * 129 * 4
+    assert size(1, 1, 8, 8, 64, 0) > 0
 
 
 def rope(lib, **over):
