@@ -104,7 +104,7 @@ struct PagedPlan {
   int pack;
   int tile_pos;                 // query positions of one 128-row tile
   int num_splits, target;
-  int64_t items, slots;         // blocks of the grid; partial results
+  int64_t tiles, items, slots;  // tiles x heads; with pieces: blocks of the grid; partial results
   size_t ws_bytes;
 };
 PagedPlan paged_plan(int batch, int total_q, int hq, int hkv, int d, int num_splits, int sms);

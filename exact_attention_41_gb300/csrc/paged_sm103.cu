@@ -45,12 +45,13 @@ using namespace sm103;
 
 constexpr int kBM = 128;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O when max grows > 256x
+constexpr int kMaxStages = 5;
 constexpr int kMinPieceSteps = 4;          // shortest piece worth a block and a partial result
 
 // NT query tiles per block, BN keys per step, as FwdCfg in the dense forward.
 template <int D, int BN, int NT>
 struct PagedCfg {
-  static constexpr int kStages = (D == 64) ? 3 : 2;
+  static constexpr int kStages = (D == 64) ? 5 : 2;
   static constexpr int kQBytes = kBM * D * 2;
   static constexpr int kKVBytes = BN * D * 2;
   static constexpr int kCols = D / 64;  // 128-byte column blocks
@@ -61,8 +62,12 @@ struct PagedCfg {
                  : (kSmemData + 1024 > 120 * 1024 ? kSmemData + 1024 : 120 * 1024);
   static constexpr int kSCol0 = NT * D;
   static constexpr uint32_t kTmemCols = kCtas == 2 ? 256 : 512;
-  static constexpr int kThreads = NT == 2 ? 384 : 192;
+  // warp 0: K producer, 1: MMA issuer.  NT = 2: warp 2 V producer, 3 idle,
+  // softmax in warps 4-11.  NT = 1: softmax in warps 2-5, warp 6 V producer.
+  static constexpr int kThreads = NT == 2 ? 384 : 224;
   static constexpr int kSoftmaxWarp0 = NT == 2 ? 4 : 2;
+  static constexpr int kSoftmaxWarps = 4 * NT;
+  static constexpr int kVWarp = NT == 2 ? 2 : 6;
   static_assert(NT * D + 2 * BN <= (int)kTmemCols, "TMEM budget");
   static_assert(kCtas == 1 || 2 * (kSmem + 1024) <= 227 * 1024, "shared memory of two blocks");
 };
@@ -95,94 +100,133 @@ __device__ __forceinline__ Steps key_steps(const PagedArgs &a, const PagedSeq &s
   return r;
 }
 
-__device__ __forceinline__ int64_t warp_sum64(int64_t x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
+__device__ __forceinline__ uint32_t add_sat(uint32_t x, uint32_t y) {
+  return min(x + y, (uint32_t)INT32_MAX);  // both at most INT32_MAX
 }
 
 // Item `idx` of the call; false behind the last one.  Whole warp; `pos` query
-// positions per block.  raise: report bad lengths (one block of the grid does).
-__device__ __forceinline__ bool find_item(const PagedArgs &a, int64_t idx, int pos, int bn,
-                                          bool raise, Item &it) {
+// positions per block.  whole: idx counts tiles, not their pieces, and the first
+// piece is found.  raise: report bad lengths (one block of the grid does).
+// Counts saturate at INT32_MAX, above every block index, so offsets that
+// overlap (more rows than total_q) only lose work, which is flagged.
+__device__ __forceinline__ bool find_item(const PagedArgs &a, uint32_t idx, int pos, int bn,
+                                          bool whole, bool raise, Item &it) {
   const int lane = threadIdx.x & 31;
   const int nh = a.pack > 1 ? a.hkv : a.hq;
   // tiles and longest key range of sequence i
-  auto shape = [&](int i, PagedSeq &s, int &mt, int &steps) {
-    mt = steps = 0;
-    if (i >= a.batch) return;
-    s = paged_seq(a, i);
-    mt = (s.lq + pos - 1) / pos;
-    if (mt == 0) return;
-    steps = max(key_steps(a, s, 0, pos, bn).nt, key_steps(a, s, (mt - 1) * pos, pos, bn).nt);
+  struct Shape {
+    PagedSeq s;
+    int tiles, steps;
   };
-  int64_t piece_steps = INT64_MAX;
-  if (a.num_splits == 0) {
-    int64_t work = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-      PagedSeq s;
-      int mt, steps;
-      shape(b0 + lane, s, mt, steps);
-      work += (int64_t)mt * steps;
+  auto shape = [&](int i) {
+    Shape x{{0, 0, 0, 0}, 0, 0};
+    if (i < a.batch) {
+      x.s = paged_seq(a, i);
+      x.tiles = (x.s.lq + pos - 1) / pos;
+      if (x.tiles > 0) x.steps = key_steps(a, x.s, (x.tiles - 1) * pos, pos, bn).nt;
+      if (x.tiles > 1) x.steps = max(x.steps, key_steps(a, x.s, 0, pos, bn).nt);
     }
-    work = warp_sum64(work) * nh;
-    piece_steps = max((int64_t)kMinPieceSteps, (work + a.target - 1) / a.target);
+    return x;
+  };
+  const Shape first = shape(lane);
+  int piece_steps = INT32_MAX;
+  if (a.num_splits == 0) {
+    // (fp32: the sums need no more than the order of magnitude, and both
+    // kernels add in the same order)
+    float work = (float)first.tiles * (float)first.steps;
+    for (int b0 = 32; b0 < a.batch; b0 += 32) {
+      const Shape x = shape(b0 + lane);
+      work += (float)x.tiles * (float)x.steps;
+    }
+    work = warp_sum(work) * (float)nh;
+    // at least work / target even after rounding, so that cut pieces fit the slots
+    piece_steps = max(kMinPieceSteps, (int)fminf(work / (float)a.target * 1.0001f, 1e9f) + 1);
   }
-  int64_t base = 0, slots = 0;
+  uint32_t base = 0, slots = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    PagedSeq s{0, 0, 0, 0};
-    int mt, steps;
-    shape(b0 + lane, s, mt, steps);
-    if (raise && s.err) raise_error(a.err, s.err);
+    const Shape x = b0 == 0 ? first : shape(b0 + lane);
+    if (raise && x.s.err) raise_error(a.err, x.s.err);
     int pieces = 1;
     if (a.num_splits == 0)
-      pieces = max(1, (int)((steps + piece_steps - 1) / piece_steps));
+      pieces = x.steps <= piece_steps ? 1 : (x.steps + piece_steps - 1) / piece_steps;
     else
-      pieces = max(1, min(a.num_splits, steps));
-    const int64_t n = (int64_t)mt * pieces * nh;
-    int64_t incl = n;
+      pieces = max(1, min(a.num_splits, x.steps));
+    const auto times = [&](int p) {
+      return (uint32_t)min((uint64_t)x.tiles * nh * p, (uint64_t)INT32_MAX);
+    };
+    const uint32_t n = times(whole ? 1 : pieces);
+    uint32_t incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += up;
+      const uint32_t up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl = add_sat(incl, up);
     }
-    const uint32_t hit = __ballot_sync(0xffffffffu, idx < base + incl);
-    const int64_t cut = pieces > 1 ? n : 0;
+    const uint32_t hit = __ballot_sync(0xffffffffu, idx < add_sat(base, incl));
+    const uint32_t cut = pieces > 1 ? times(pieces) : 0;  // slots
     if (hit) {
       const int src = __ffs(hit) - 1;
-      slots += warp_sum64(lane < src ? cut : 0);
-      const int local = (int)(idx - base - __shfl_sync(0xffffffffu, incl - n, src));
+      slots = add_sat(slots, __reduce_add_sync(0xffffffffu, lane < src ? cut : 0));
+      const uint32_t local = idx - base - __shfl_sync(0xffffffffu, incl - n, src);
       it.seq = b0 + src;
       it.pieces = __shfl_sync(0xffffffffu, pieces, src);
-      const int tiles = __shfl_sync(0xffffffffu, mt, src);
-      it.s.q0 = __shfl_sync(0xffffffffu, s.q0, src);
-      it.s.lq = __shfl_sync(0xffffffffu, s.lq, src);
-      it.s.lk = __shfl_sync(0xffffffffu, s.lk, src);
+      const int tiles = __shfl_sync(0xffffffffu, x.tiles, src);
+      it.s.q0 = __shfl_sync(0xffffffffu, x.s.q0, src);
+      it.s.lq = __shfl_sync(0xffffffffu, x.s.lq, src);
+      it.s.lk = __shfl_sync(0xffffffffu, x.s.lk, src);
       it.s.err = 0;
       // heads fastest (they share a sequence's pages and, in L2, its K and V),
       // then pieces; the last positions, which see the most keys, first
-      it.head = local % nh;
-      it.piece = local / nh % it.pieces;
-      it.m0 = (tiles - 1 - local / nh / it.pieces) * pos;
-      it.slot = it.pieces > 1 ? (int)(slots + local) : -1;
-      return true;
+      const uint32_t upper = local / (uint32_t)nh;
+      it.head = (int)(local - upper * nh);
+      const uint32_t m = whole ? upper : upper / (uint32_t)it.pieces;
+      it.piece = whole ? 0 : (int)(upper - m * it.pieces);
+      it.m0 = (tiles - 1 - (int)m) * pos;
+      // pieces of one tile and head are nh slots apart
+      const uint32_t at = (m * it.pieces + it.piece) * nh + it.head;
+      it.slot = it.pieces > 1 ? (int)add_sat(slots, at) : -1;
+      return it.m0 >= 0;
     }
-    base += __shfl_sync(0xffffffffu, incl, 31);
-    slots += warp_sum64(cut);
+    base = add_sat(base, __shfl_sync(0xffffffffu, incl, 31));
+    slots = add_sat(slots, __reduce_add_sync(0xffffffffu, cut));
   }
   return false;
 }
 
+// One piece of an item in key steps.
+struct Piece {
+  int n_lo, nt;     // first step and how many
+  int kb, ke;       // visible keys of the block's rows (of all pieces)
+  int front, back;  // V rows of the first / last step outside [kb, ke)
+  int live;         // 0: behind the last item, or behind the last key (the
+                    // combine step skips such a piece by the same test)
+};
+__device__ __forceinline__ Piece piece_of(const PagedArgs &a, const Item &it, int pos, int bn,
+                                          bool found) {
+  const Steps all = key_steps(a, it.s, it.m0, pos, bn);
+  const int per = it.pieces > 1 ? (all.nt + it.pieces - 1) / it.pieces : all.nt;
+  const int lo = min(it.piece * per, all.nt);
+  Piece p;
+  p.live = found && (it.piece == 0 || lo < all.nt);
+  p.n_lo = all.n_lo + lo;
+  p.nt = p.live ? min(all.nt - lo, per) : 0;
+  p.kb = all.kb;
+  p.ke = all.ke;
+  p.front = p.nt > 0 ? max(0, all.kb - p.n_lo * bn) : 0;
+  p.back = p.nt > 0 ? max(0, (p.n_lo + p.nt) * bn - all.ke) : 0;
+  return p;
+}
+
 struct Shared {
   uint64_t q_full;
-  uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3];
+  uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t v_clean[2];  // first / last V tile: rows that no query sees are zeroed
   uint64_t all_done;    // every MMA of the block has completed
   uint64_t wait_ns;
   Item item;
+  Piece piece;
   uint32_t tmem_base;
-  int live, abort;
+  int abort;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -218,96 +262,103 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pg = a.pack;
+  // the combine kernel may start to find its tiles as soon as there is room
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 0) {
     Item it{};
     it.pieces = 1;
-    const bool live = find_item(a, blockIdx.x, tile_pos * NT, BN, blockIdx.x == 0, it);
+    const bool found = find_item(a, blockIdx.x, tile_pos * NT, BN, false, blockIdx.x == 0, it);
+    const Piece p = piece_of(a, it, tile_pos * NT, BN, found);
     if (lane == 0) {
       sh.item = it;
-      sh.live = live;
-      mbar_init(&sh.q_full, 1);
-      for (int s = 0; s < ST; ++s) {
-        mbar_init(&sh.k_full[s], 1);
-        mbar_init(&sh.k_empty[s], 1);
-        mbar_init(&sh.v_full[s], 1);
-        mbar_init(&sh.v_empty[s], 1);
-      }
+      sh.piece = p;
       // softmax threads that take part: warps with a row of the sequence
       for (int s = 0; s < 2; ++s) {
         const int t = NT == 2 ? s : 0;
         const int rows = min(max(it.s.lq - it.m0 - t * tile_pos, 0), tile_pos) * pg;
-        mbar_init(&sh.s_full[s], 1);
         mbar_init(&sh.p_full[s], max(1, (rows + 31) / 32 * 32));
-        mbar_init(&sh.o_done[s], 1);
-        mbar_init(&sh.v_clean[s], 1);
       }
-      mbar_init(&sh.all_done, 1);
-      sh.wait_ns = a.wait_ns;
-      sh.abort = 0;
       fence_mbar_init();
     }
   } else if (warp == 1) {
     tmem_alloc(&sh.tmem_base, C::kTmemCols);
     tmem_relinquish();
+  } else if (threadIdx.x == C::kVWarp * 32) {
+    mbar_init(&sh.q_full, 1);
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&sh.k_full[s], 1);
+      mbar_init(&sh.k_empty[s], 1);
+      mbar_init(&sh.v_full[s], 1);
+      mbar_init(&sh.v_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sh.s_full[s], 1);
+      mbar_init(&sh.o_done[s], 1);
+      mbar_init(&sh.v_clean[s], 1);
+    }
+    mbar_init(&sh.all_done, 1);
+    sh.wait_ns = a.wait_ns;
+    sh.abort = 0;
+    prefetch_tmap(&tq);
+    prefetch_tmap(&tk);
+    prefetch_tmap(&tv);
+    fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
   const Item it = sh.item;
+  const Piece pc = sh.piece;
   const PagedSeq sq = it.s;
   const int kvh = pg > 1 ? it.head : it.head / (a.hq / a.hkv);
   const int h = pg > 1 ? kvh * pg : it.head;  // (first) query head of the rows
-
-  // The block's key steps, and this piece of them.
-  const Steps all = key_steps(a, sq, it.m0, tile_pos * NT, BN);
-  const int per = (all.nt + it.pieces - 1) / it.pieces;
-  const int p_lo = min(it.piece * per, all.nt);
-  // behind the last item, or a piece behind the last key (the combine step
-  // skips it by the same test): nothing to do
-  const bool live = sh.live && (it.piece == 0 || p_lo < all.nt);
-  const int n_lo = all.n_lo + p_lo;                             // first step of the piece
-  const int nt = live ? min(all.nt - p_lo, per) : 0;            // and how many
+  const int n_lo = pc.n_lo, nt = pc.nt, front = pc.front, back = pc.back;
+  const bool live = pc.live;
   // steps [ta, tb) of the piece that tile t takes part in: those with a key
   // that one of its rows sees
   auto tile_steps = [&](int t, int &ta, int &tb) {
-    const Steps x = key_steps(a, sq, it.m0 + t * tile_pos, tile_pos, BN);
-    ta = min(max(x.n_lo - n_lo, 0), nt);
-    tb = min(max(x.n_lo + x.nt - n_lo, ta), nt);
-    if (x.nt == 0) ta = tb = 0;
+    ta = 0;
+    tb = nt;
+    if constexpr (NT == 2) {
+      const Steps x = key_steps(a, sq, it.m0 + t * tile_pos, tile_pos, BN);
+      ta = min(max(x.n_lo - n_lo, 0), nt);
+      tb = min(max(x.n_lo + x.nt - n_lo, ta), nt);
+      if (x.nt == 0) ta = tb = 0;
+    }
   };
-  // V rows of the piece's first and last step that lie outside [kb, ke)
-  const int front = nt > 0 ? max(0, all.kb - n_lo * BN) : 0;
-  const int back = nt > 0 ? max(0, (n_lo + nt) * BN - all.ke) : 0;
 
-  if (warp < C::kSoftmaxWarp0) {
+  if (warp < C::kSoftmaxWarp0 || warp >= C::kSoftmaxWarp0 + C::kSoftmaxWarps) {
     if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
-    if (warp == 0) {
-      // ---------------------------------------------------------- producer
+    if (warp == 0 || warp == C::kVWarp) {
+      // ----------------------------------------- producers: warp 0 K, kVWarp V
       if (nt > 0) {
-        const int boxes = BN / box_rows;
-        const int box = lane / C::kCols, col = lane % C::kCols;
-        // this lane's box of step j: page (-1: not needed, -2: outside the
-        // pool) and slot
-        auto locate = [&](int j, int &page, int &slot) {
-          const int row0 = (n_lo + j) * BN + box * box_rows;
-          page = -1;
-          slot = 0;
-          if (box < boxes && j < nt && row0 < all.ke && row0 + box_rows > all.kb) {
-            const int lp = a.block_table ? row0 / a.page_size : 0;
-            slot = row0 - lp * a.page_size;
-            page = paged_page(a, it.seq, lp);
-            if (page < 0) page = -2;
-          }
+        const bool is_v = warp != 0;
+        const CUtensorMap *map = is_v ? &tv : &tk;
+        uint64_t *full = is_v ? sh.v_full : sh.k_full, *empty = is_v ? sh.v_empty : sh.k_empty;
+        const int boxes = BN / box_rows;  // a power of two
+        const int box = lane / C::kCols, col = lane % C::kCols;  // this lane's part of a tile
+        const int key_lo = n_lo * BN;
+        uint8_t *dst = (is_v ? v_s : k_s) + col * (BN * 128) + box * box_rows * 128;
+        // Pages and slots of 32 boxes at a time, one per lane, and of the next
+        // 32 ahead: a look-up per step would add a trip to L2 or further to it.
+        struct Box {
+          int page, slot;  // page -1: no visible key, -2: outside the pool
         };
-        int page, slot;
-        locate(0, page, slot);
-        if (lane == 0) {
-          prefetch_tmap(&tq);
-          prefetch_tmap(&tk);
-          prefetch_tmap(&tv);
-          const int q_rows = tile_pos * pg;
-          mbar_expect_tx(&sh.q_full, NT * q_rows * D * 2);
+        auto fetch = [&](int b0) {
+          Box x{-1, 0};
+          const int row0 = key_lo + (b0 + lane) * box_rows;
+          if (b0 + lane < nt * boxes && row0 < pc.ke && row0 + box_rows > pc.kb) {
+            const int lp = a.block_table ? row0 / a.page_size : 0;
+            x.slot = row0 - lp * a.page_size;
+            x.page = paged_page(a, it.seq, lp);
+            if (x.page < 0) x.page = -2;
+          }
+          return x;
+        };
+        Box now{-1, 0}, ahead = fetch(0);
+        if (!is_v && lane == 0) {
+          mbar_expect_tx(&sh.q_full, NT * tile_pos * pg * D * 2);
           for (int t = 0; t < NT; ++t)
             for (int c = 0; c < C::kCols; ++c)
               tma_load_3d(q_s + t * C::kQBytes + c * kBM * 128, &tq, &sh.q_full, c * 64, h,
@@ -326,44 +377,45 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
           __syncwarp();
           if (lane == 0) mbar_arrive(bar);
         };
-        const int front_after = min(ST, nt) - 1;  // step after whose loads the first tile is cleaned
-        int issued = 0;                            // K and V loads: 2 per step
+        const int front_after = min(ST, nt) - 1;  // step after whose load the first tile is cleaned
+        int issued = 0;
         for (int j = 0; j < nt; ++j) {
           const int st = j % ST;
-          const uint32_t ph = ((j / ST) & 1) ^ 1;
-          if (__any_sync(0xffffffffu, page == -2)) {
-            if (lane == 0) {
-              raise_error(a.err, kErrPageOutOfRange);
-              *(volatile int *)&sh.abort = 1;
+          const int in32 = j * boxes % 32;
+          if (in32 == 0) {
+            now = ahead;
+            if (__any_sync(0xffffffffu, now.page == -2)) {
+              if (lane == 0) {
+                raise_error(a.err, kErrPageOutOfRange);
+                *(volatile int *)&sh.abort = 1;
+              }
+              break;
             }
-            break;
+            ahead = fetch(j * boxes + 32);
           }
-          const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, page >= 0)) * box_rows * 128;
-          const int pnow = page, snow = slot;
-          locate(j + 1, page, slot);
-          const int dst = st * C::kKVBytes + col * (BN * 128) + box * box_rows * 128;
-          if (!wait_warp(sh, &sh.k_empty[st], ph, a.err)) break;
-          if (lane == 0) mbar_expect_tx(&sh.k_full[st], bytes);
-          __syncwarp();
-          if (pnow >= 0) tma_load_4d(k_s + dst, &tk, &sh.k_full[st], col * 64, kvh, snow, pnow);
-          issued = 2 * j + 1;
-          if (!wait_warp(sh, &sh.v_empty[st], ph, a.err)) break;
-          if (lane == 0) mbar_expect_tx(&sh.v_full[st], bytes);
-          __syncwarp();
-          if (pnow >= 0) tma_load_4d(v_s + dst, &tv, &sh.v_full[st], col * 64, kvh, snow, pnow);
-          issued = 2 * j + 2;
-          if (j == front_after && front > 0) clean(0, 0, min(front, BN), &sh.v_clean[0]);
+          const int page = __shfl_sync(0xffffffffu, now.page, (in32 + box) & 31);
+          const int slot = __shfl_sync(0xffffffffu, now.slot, (in32 + box) & 31);
+          const bool load = box < boxes && page >= 0;
+          const uint32_t bytes =
+              (uint32_t)__popc(__ballot_sync(0xffffffffu, load)) * box_rows * 128;
+          bool ok = true;
+          if (lane == 0) {
+            ok = wait_bar(sh, &empty[st], ((j / ST) & 1) ^ 1, a.err);
+            if (ok) mbar_expect_tx(&full[st], bytes);
+          }
+          if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+          if (load) tma_load_4d(dst + st * C::kKVBytes, map, &full[st], col * 64, kvh, slot, page);
+          issued = j + 1;
+          if (is_v && j == front_after && front > 0) clean(0, 0, min(front, BN), &sh.v_clean[0]);
         }
-        if (issued == 2 * nt && back > 0) clean(nt - 1, BN - back, BN, &sh.v_clean[1]);
+        if (is_v && issued == nt && back > 0) clean(nt - 1, BN - back, BN, &sh.v_clean[1]);
         __syncwarp();
         if (*(volatile int *)&sh.abort) {
-          // let this block's copies in flight land before it exits
+          // let this warp's copies in flight land before the block exits
           int *noerr = nullptr;
-          mbar_wait(&sh.q_full, 0, noerr);
-          for (int x = max(0, issued - 2 * ST); x < issued; ++x) {
-            const int j = x / 2, st = j % ST;
-            mbar_wait(x % 2 ? &sh.v_full[st] : &sh.k_full[st], (j / ST) & 1, noerr);
-          }
+          if (!is_v) mbar_wait(&sh.q_full, 0, noerr);
+          for (int j = max(0, issued - ST); j < issued; ++j)
+            mbar_wait(&full[j % ST], (j / ST) & 1, noerr);
         }
       }
     } else if (warp == 1) {
@@ -535,16 +587,30 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
         }
         // softcap, then the mask
         if (cap) {
-          // c tanh(x cap_in) in log2 units = cap_out - 2 cap_out / (e^{2 x cap_in} + 1)
+          // c tanh(x cap_in) in log2 units = cap_out - 2 cap_out / y with
+          // y = e^{2 x cap_in} + 1.  One reciprocal serves four scores:
+          // 1 / y0 = y1 (y2 y3) / (y0 y1 y2 y3).  The exponent is held to 2^30,
+          // where tanh rounds to 1, so that the product stays finite.
           const uint64_t k2 = f2_pack(cap_k, cap_k), one2 = f2_pack(1.f, 1.f);
           const uint64_t co2 = f2_pack(cap_out, cap_out);
           const uint64_t mco2 = f2_pack(-2.f * cap_out, -2.f * cap_out);
 #pragma unroll
-          for (int e = 0; e < BN; e += 2) {
-            float a0, a1, y0, y1;
+          for (int e = 0; e < BN; e += 4) {
+            float a0, a1, a2, a3;
             f2_unpack(f2_mul(f2_pack(x[e], x[e + 1]), k2), a0, a1);
-            f2_unpack(f2_add(f2_pack(ex2(a0), ex2(a1)), one2), y0, y1);
-            f2_unpack(f2_fma(f2_pack(rcp_approx(y0), rcp_approx(y1)), mco2, co2), x[e], x[e + 1]);
+            f2_unpack(f2_mul(f2_pack(x[e + 2], x[e + 3]), k2), a2, a3);
+            const uint64_t y01 = f2_add(f2_pack(ex2(fminf(a0, 30.f)), ex2(fminf(a1, 30.f))), one2);
+            const uint64_t y23 = f2_add(f2_pack(ex2(fminf(a2, 30.f)), ex2(fminf(a3, 30.f))), one2);
+            float y0, y1, y2, y3, pa, pb;
+            f2_unpack(y01, y0, y1);
+            f2_unpack(y23, y2, y3);
+            f2_unpack(f2_mul(f2_pack(y0, y2), f2_pack(y1, y3)), pa, pb);  // y0 y1, y2 y3
+            const float r = rcp_approx(pa * pb);
+            const float ra = r * pb, rb = r * pa;                         // 1 / (y0 y1), 1 / (y2 y3)
+            const uint64_t i01 = f2_mul(f2_pack(ra, ra), f2_pack(y1, y0));
+            const uint64_t i23 = f2_mul(f2_pack(rb, rb), f2_pack(y3, y2));
+            f2_unpack(f2_fma(i01, mco2, co2), x[e], x[e + 1]);
+            f2_unpack(f2_fma(i23, mco2, co2), x[e + 2], x[e + 3]);
           }
         }
         if (key0 < lo_tile_max || key0 + BN - 1 > hi_tile_min) {
@@ -604,22 +670,23 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
           l += ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
         }
         tmem_wait_st();
-        if (j > 0) {
-          // O holds P_{j-1} V_{j-1} once this completes; only then may it be rescaled
+        if (j > 0 && __any_sync(0xffffffffu, rescale)) {
+          // O holds P_{j-1} V_{j-1} once this completes; only then may it be
+          // rescaled.  (Without a rescale there is nothing to wait for: P_j has
+          // its own columns, and the product that reads it is issued later.  The
+          // parity cannot be mistaken: step j's product needs this warp's P.)
           if (!wait_warp(sh, &sh.o_done[t], (j - 1) & 1, a.err)) { ok = false; break; }
           tc_fence_after();
-          if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t u[32];
-              tmem_ld32(o_t + c * 32, u);
-              tmem_wait_ld();
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t u[32];
+            tmem_ld32(o_t + c * 32, u);
+            tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
-              tmem_st32(o_t + c * 32, u);
-            }
-            tmem_wait_st();
+            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+            tmem_st32(o_t + c * 32, u);
           }
+          tmem_wait_st();
         }
         tc_fence_before();
         mbar_arrive(&sh.p_full[sb]);
@@ -682,7 +749,7 @@ constexpr int kCombineWarps = 4;
 
 // Joins the pieces of cut rows, one warp per row: with l_p the log2-sums,
 // L = log2 sum 2^l_p and O = sum 2^(l_p - L) O_p, in piece order.  One block per
-// item and row group; the first piece's block of a tile does the work.
+// tile, head and row group.
 template <typename T, int D, int BN, int NT>
 __global__ void __launch_bounds__(kCombineWarps * 32)
     paged_combine_kernel(const PagedArgs a, const int tile_pos) {
@@ -693,20 +760,23 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   if (warp == 0) {
     Item it{};
     it.pieces = 1;
-    const bool l = find_item(a, blockIdx.x, tile_pos * NT, BN, false, it);
+    const bool found = find_item(a, blockIdx.x, tile_pos * NT, BN, true, false, it);
     if (lane == 0) {
       item = it;
-      live = l && it.piece == 0 && it.pieces > 1;
+      live = found && it.pieces > 1;
     }
   }
   __syncthreads();
+  // Launched while the blocks of paged_tc_kernel still run: from here on they
+  // have all finished and their results can be read.  Every thread waits, so
+  // that this grid, and with it the call, does not end before that one.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!live) return;
   const Item it = item;
   const int pg = a.pack, nh = pg > 1 ? a.hkv : a.hq;
   const Steps all = key_steps(a, it.s, it.m0, tile_pos * NT, BN);
   const int per = (all.nt + it.pieces - 1) / it.pieces;
-  const int n = max(1, all.nt == 0 ? 1 : (all.nt + per - 1) / per);  // pieces that were written
-  // pieces of one tile and head are nh slots apart
+  const int n = all.nt == 0 ? 1 : (all.nt + per - 1) / per;  // pieces that were written
   if ((int64_t)it.slot + (int64_t)(n - 1) * nh >= a.slots) return;
   for (int x = blockIdx.y * kCombineWarps + warp; x < NT * tile_pos * pg;
        x += gridDim.y * kCombineWarps) {
@@ -787,9 +857,17 @@ cudaError_t paged(const PagedArgs &a, const PagedPlan &plan, cudaStream_t st) {
   count_launches(1);
   if (a.num_splits != 1) {
     const int64_t rows = std::max<int64_t>(1, (int64_t)a.total_q * a.pack / a.batch);
-    const int groups = (int)std::min<int64_t>(NT * 8, (rows + 15) / 16);
-    paged_combine_kernel<T, D, BN, NT><<<dim3((unsigned)plan.items, groups), kCombineWarps * 32, 0, st>>>(
-        a, plan.tile_pos);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)plan.tiles, (unsigned)std::min<int64_t>(NT * 8, (rows + 15) / 16));
+    cfg.blockDim = dim3(kCombineWarps * 32);
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, paged_combine_kernel<T, D, BN, NT>, a, plan.tile_pos);
+    if (e != cudaSuccess) return e;
     count_launches(1);
   }
   return cudaGetLastError();
@@ -814,7 +892,7 @@ PagedPlan paged_plan(int batch, int total_q, int hq, int hkv, int d, int num_spl
   const int pos = p.tile_pos * p.layout;
   const int64_t wave = (int64_t)sms * (p.layout == 1 && d <= 128 ? 2 : 1);
   // sum of ceil(n_i / pos) over sequences of sum total_q
-  const int64_t tiles = (total_q / pos + std::min(batch, total_q)) * (int64_t)nh;
+  p.tiles = (total_q / pos + std::min(batch, total_q)) * (int64_t)nh;
   p.num_splits = num_splits;
   // enough tiles for several waves even if no sequence leaves one half empty
   if (num_splits == 0 && (int64_t)(total_q + pos - 1) / pos * nh >= 4 * wave) p.num_splits = 1;
@@ -822,10 +900,10 @@ PagedPlan paged_plan(int batch, int total_q, int hq, int hkv, int d, int num_spl
   if (p.num_splits == 0) {
     // cut pieces: below 2 target (each cut tile has at least one piece of full
     // length, and full pieces are at most target)
-    p.items = tiles + p.target;
+    p.items = p.tiles + p.target;
     p.slots = std::min<int64_t>(2 * (int64_t)p.target, p.items);
   } else {
-    p.items = tiles * p.num_splits;
+    p.items = p.tiles * p.num_splits;
     p.slots = p.num_splits > 1 ? p.items : 0;
   }
   p.ws_bytes = (size_t)p.slots * kBM * p.layout * (d + 1) * sizeof(float);

@@ -119,11 +119,11 @@ def _dt(t) -> int:
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream():
-    return ctypes.c_void_p(_torch().cuda.current_stream().cuda_stream)
+    return _torch().cuda.current_stream().cuda_stream
 
 
 def _need(cond, msg):
@@ -414,20 +414,41 @@ def fwd_fp8(q, k, v, descale_q=1.0, descale_k=1.0, descale_v=1.0, *, scale=None,
 
 # ------------------------------------------- ragged chunks over a paged cache
 
+class _Same:
+    """No device change: the tensors' device is current already."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_SAME = _Same()
+
+
 def _on_device(*ts):
     """The tensors lie on one CUDA device; a guard that makes it current (the
     calls below then run on that device's current stream)."""
     torch = _torch()
-    ts = [t for t in ts if t is not None]
+    index = None
     for t in ts:
-        _need(t.is_cuda, "tensors must be on a CUDA device")
-        _need(t.device == ts[0].device, "tensors must be on one device")
-    return torch.cuda.device(ts[0].device)
+        if t is not None:
+            _need(t.is_cuda, "tensors must be on a CUDA device")
+            i = t.get_device()
+            _need(index is None or i == index, "tensors must be on one device")
+            index = i
+    return _SAME if index == torch.cuda.current_device() else torch.cuda.device(index)
+
+
+def _contig(*ts):
+    for t in ts:
+        _need(t is None or t.is_contiguous(), "tensors must be contiguous")
 
 
 def _like(t, ref, shape, what):
     _need(t.dtype == ref.dtype, f"{what} must have the dtype of the queries or keys")
-    _need(tuple(t.shape) == tuple(shape), f"{what} must have shape {tuple(shape)}")
+    _need(t.shape == shape, f"{what} must have shape {tuple(shape)}")
 
 
 def _packed_stride(t):
@@ -453,19 +474,21 @@ def _page_stride(t):
 
 
 def _cache_args(k_cache, v_cache, cu_seqlens, cache_seqlens, block_table):
+    """(batch, num_pages, page_size, max_pages) after the checks of a cache."""
+    i32 = _torch().int32
     _need(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype,
           "k_cache and v_cache must be (num_pages, page_size, hkv, d) of one dtype")
     batch = cache_seqlens.numel()
-    _need(cu_seqlens.dtype == _torch().int32 and cache_seqlens.dtype == _torch().int32,
+    _need(cu_seqlens.dtype == i32 and cache_seqlens.dtype == i32,
           "cu_seqlens and cache_seqlens must be int32")
     _need(cu_seqlens.numel() == batch + 1, "cu_seqlens must have one entry more than cache_seqlens")
     num_pages, page_size = k_cache.shape[:2]
     max_pages = 1
     if block_table is not None:
-        _need(block_table.dtype == _torch().int32 and block_table.dim() == 2 and
+        _need(block_table.dtype == i32 and block_table.dim() == 2 and
               block_table.shape[0] == batch, "block_table must be int32 (batch, max_pages)")
         max_pages = block_table.shape[1]
-    _cuda_contig(cu_seqlens, cache_seqlens, block_table)
+    _contig(cu_seqlens, cache_seqlens, block_table)
     return batch, num_pages, page_size, max_pages
 
 
@@ -498,7 +521,7 @@ def fwd_paged(q, k_cache, v_cache, cu_seqlens_q, cache_seqlens, *, block_table=N
     _need(tuple(lse.shape) == (hq, rows) and lse.dtype == torch.float32, "lse must be (hq, Tq) fp32")
     ws = paged_workspace(q, k_cache, batch, num_splits) if workspace is None else workspace
     strides = (_packed_stride(q), _page_stride(k_cache), _page_stride(v_cache))
-    _cuda_contig(out, lse, ws)
+    _contig(out, lse, ws)
     wl, wr = _win(window)
     with _on_device(q, k_cache, v_cache, cu_seqlens_q, cache_seqlens, block_table, out, lse, ws):
         st = lib().attn_fwd_paged(_p(q), _p(k_cache), _p(v_cache), _p(out), _p(lse), *strides,
@@ -533,11 +556,11 @@ def _rope_args(phases, q_weight, k_weight, ref):
     if phases is not None:
         _need(phases.dtype == torch.int64 and phases.dim() == 1, "phases must be 1-D int64 (rope_phases)")
         _need(2 * phases.numel() <= ref.shape[-1], "more rotation pairs than half of the head")
-        _cuda_contig(phases)
+        _contig(phases)
     for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
             _like(w, ref, (ref.shape[-1],), n)
-            _cuda_contig(w)
+            _contig(w)
     return _p(phases), 0 if phases is None else 2 * phases.numel()
 
 
@@ -562,7 +585,7 @@ def _positions(positions, b, s):
     if positions is not None:
         _need(positions.dtype == _torch().int32 and positions.numel() == b * s,
               "positions must be int32 with one entry per token")
-        _cuda_contig(positions)
+        _contig(positions)
     return _p(positions)
 
 
@@ -630,7 +653,7 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, *, phases=None, positions=None, inter
             _like(w, ref, (d,), n)
     ws = qk_norm_rope_bwd_workspace(q, k) if workspace is None else workspace
     ph, rot = _rope_args(phases, q_weight, k_weight, ref)
-    _cuda_contig(dq_out, dk_out, dq_weight, dk_weight, ws)
+    _contig(dq_out, dk_out, dq_weight, dk_weight, ws)
     rs = [_row_stride(t) for t in (q, k, dq, dk)]
     with _on_device(q, k, dq_out, dk_out, dq, dk, phases, positions, q_weight, k_weight, dq_weight,
                     dk_weight, ws):
@@ -663,7 +686,7 @@ def kvcache_append(k_new, v_new, k_cache, v_cache, cu_seqlens, cache_seqlens, *,
         _like(q, k_new, (total, hq, d), "q")
         q_out = torch.empty_like(q, memory_format=torch.contiguous_format) if q_out is None else q_out
         _like(q_out, q, q.shape, "q_out")
-        _cuda_contig(q_out)
+        _contig(q_out)
     ph, rot = _rope_args(phases, q_weight, k_weight, k_new)
     rs = [_packed_stride(t) for t in (q, k_new, v_new)]
     with _on_device(k_new, v_new, k_cache, v_cache, cu_seqlens, cache_seqlens, block_table, q,
