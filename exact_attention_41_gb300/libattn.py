@@ -103,10 +103,17 @@ def _check(status: int, what: str):
         raise AttnError(status, what)
 
 
-def _torch():
-    import torch
+_torch_module = None
 
-    return torch
+
+def _torch():
+    """torch, imported at the first use (host-only calls do without it)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def _dt(t) -> int:
@@ -123,7 +130,12 @@ def _p(t):
 
 
 def _stream():
-    return _torch().cuda.current_stream().cuda_stream
+    """Handle of the current device's current stream."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return torch.cuda.current_stream().cuda_stream
+    return raw(torch.cuda.current_device())  # without building a Stream object: 3 us less a call
 
 
 def _need(cond, msg):
@@ -413,6 +425,8 @@ def fwd_fp8(q, k, v, descale_q=1.0, descale_k=1.0, descale_v=1.0, *, scale=None,
 
 
 # ------------------------------------------- ragged chunks over a paged cache
+# (The checks below are written out, with their messages made only when they
+# fail: on small calls the host's time is the call's time.)
 
 class _Same:
     """No device change: the tensors' device is current already."""
@@ -430,25 +444,31 @@ _SAME = _Same()
 def _on_device(*ts):
     """The tensors lie on one CUDA device; a guard that makes it current (the
     calls below then run on that device's current stream)."""
-    torch = _torch()
     index = None
     for t in ts:
         if t is not None:
-            _need(t.is_cuda, "tensors must be on a CUDA device")
             i = t.get_device()
-            _need(index is None or i == index, "tensors must be on one device")
-            index = i
-    return _SAME if index == torch.cuda.current_device() else torch.cuda.device(index)
+            if i != index:
+                if i < 0:
+                    raise ValueError("tensors must be on a CUDA device")
+                if index is not None:
+                    raise ValueError("tensors must be on one device")
+                index = i
+    cuda = _torch().cuda
+    return _SAME if index == cuda.current_device() else cuda.device(index)
 
 
 def _contig(*ts):
     for t in ts:
-        _need(t is None or t.is_contiguous(), "tensors must be contiguous")
+        if t is not None and not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
 
 
 def _like(t, ref, shape, what):
-    _need(t.dtype == ref.dtype, f"{what} must have the dtype of the queries or keys")
-    _need(t.shape == shape, f"{what} must have shape {tuple(shape)}")
+    if t.dtype != ref.dtype:
+        raise ValueError(f"{what} must share the dtype of the queries or keys")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}")
 
 
 def _packed_stride(t):
@@ -476,17 +496,18 @@ def _page_stride(t):
 def _cache_args(k_cache, v_cache, cu_seqlens, cache_seqlens, block_table):
     """(batch, num_pages, page_size, max_pages) after the checks of a cache."""
     i32 = _torch().int32
-    _need(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype,
-          "k_cache and v_cache must be (num_pages, page_size, hkv, d) of one dtype")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise ValueError("k_cache and v_cache must be (num_pages, page_size, hkv, d) of one dtype")
     batch = cache_seqlens.numel()
-    _need(cu_seqlens.dtype == i32 and cache_seqlens.dtype == i32,
-          "cu_seqlens and cache_seqlens must be int32")
-    _need(cu_seqlens.numel() == batch + 1, "cu_seqlens must have one entry more than cache_seqlens")
-    num_pages, page_size = k_cache.shape[:2]
+    if cu_seqlens.dtype != i32 or cache_seqlens.dtype != i32:
+        raise ValueError("cu_seqlens and cache_seqlens must be int32")
+    if cu_seqlens.numel() != batch + 1:
+        raise ValueError("cu_seqlens must have one entry more than cache_seqlens")
+    num_pages, page_size, _, _ = k_cache.shape
     max_pages = 1
     if block_table is not None:
-        _need(block_table.dtype == i32 and block_table.dim() == 2 and
-              block_table.shape[0] == batch, "block_table must be int32 (batch, max_pages)")
+        if block_table.dtype != i32 or block_table.dim() != 2 or block_table.shape[0] != batch:
+            raise ValueError("block_table must be int32 (batch, max_pages)")
         max_pages = block_table.shape[1]
     _contig(cu_seqlens, cache_seqlens, block_table)
     return batch, num_pages, page_size, max_pages
@@ -494,11 +515,11 @@ def _cache_args(k_cache, v_cache, cu_seqlens, cache_seqlens, block_table):
 
 def paged_workspace(q, k_cache, batch, num_splits=0):
     """Scratch memory of fwd_paged for these queries and this cache."""
-    torch = _torch()
     rows, hq, d = q.shape
     with _on_device(q):
         n = lib().attn_fwd_paged_workspace_size(int(batch), rows, hq, k_cache.shape[2], d,
                                                 int(num_splits))
+    torch = _torch()
     return torch.empty(max(n, 1), device=q.device, dtype=torch.uint8)
 
 
@@ -513,23 +534,30 @@ def fwd_paged(q, k_cache, v_cache, cu_seqlens_q, cache_seqlens, *, block_table=N
     rows, hq, d = q.shape
     batch, num_pages, page_size, max_pages = _cache_args(k_cache, v_cache, cu_seqlens_q,
                                                          cache_seqlens, block_table)
-    _need(k_cache.dtype == q.dtype and k_cache.shape[3] == d, "q and the cache must share dtype and d")
     hkv = k_cache.shape[2]
-    out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
-    lse = torch.empty((hq, rows), device=q.device, dtype=torch.float32) if lse is None else lse
-    _like(out, q, q.shape, "out")
-    _need(tuple(lse.shape) == (hq, rows) and lse.dtype == torch.float32, "lse must be (hq, Tq) fp32")
-    ws = paged_workspace(q, k_cache, batch, num_splits) if workspace is None else workspace
-    strides = (_packed_stride(q), _page_stride(k_cache), _page_stride(v_cache))
-    _contig(out, lse, ws)
-    wl, wr = _win(window)
-    with _on_device(q, k_cache, v_cache, cu_seqlens_q, cache_seqlens, block_table, out, lse, ws):
-        st = lib().attn_fwd_paged(_p(q), _p(k_cache), _p(v_cache), _p(out), _p(lse), *strides,
+    if k_cache.dtype != q.dtype or k_cache.shape[3] != d:
+        raise ValueError("q and the cache must share dtype and d")
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        _like(out, q, q.shape, "out")
+    if lse is None:
+        lse = torch.empty((hq, rows), device=q.device, dtype=torch.float32)
+    elif lse.shape != (hq, rows) or lse.dtype != torch.float32:
+        raise ValueError("lse must be (hq, Tq) fp32")
+    if workspace is None:
+        workspace = paged_workspace(q, k_cache, batch, num_splits)
+    _contig(out, lse, workspace)
+    wl, wr = window
+    with _on_device(q, k_cache, v_cache, cu_seqlens_q, cache_seqlens, block_table, out, lse,
+                    workspace):
+        st = lib().attn_fwd_paged(_p(q), _p(k_cache), _p(v_cache), _p(out), _p(lse),
+                                  _packed_stride(q), _page_stride(k_cache), _page_stride(v_cache),
                                   _p(cu_seqlens_q), _p(cache_seqlens), _p(block_table), num_pages,
-                                  page_size, max_pages, int(bool(appended)), batch, rows, _dt(q),
-                                  hq, hkv, d, _scale(scale, d), int(bool(causal)), wl, wr,
-                                  float(softcap), int(num_splits), _p(ws),
-                                  ws.numel() * ws.element_size(), _stream())
+                                  page_size, max_pages, 1 if appended else 0, batch, rows, _dt(q),
+                                  hq, hkv, d, _scale(scale, d), 1 if causal else 0, int(wl),
+                                  int(wr), softcap, num_splits, _p(workspace), workspace.nbytes,
+                                  _stream())
     _check(st, "attn_fwd_paged")
     return out, lse
 
@@ -544,49 +572,66 @@ def rope_phases(inv_freq, device=None):
     f = torch.as_tensor(inv_freq, dtype=torch.float64)
     if device is None:
         device = f.device if f.is_cuda else torch.device("cuda", torch.cuda.current_device())
-    bits = [lib().attn_rope_phase(float(x)) for x in f.flatten().cpu()]
-    _need(all(math.isfinite(float(x)) for x in f.flatten().cpu()), "frequencies must be finite")
+    values = f.flatten().tolist()
+    _need(all(math.isfinite(x) for x in values), "frequencies must be finite")
+    bits = [lib().attn_rope_phase(x) for x in values]
     return torch.tensor([b - (1 << 64) if b >= 1 << 63 else b for b in bits], dtype=torch.int64,
                         device=device)
 
 
 def _rope_args(phases, q_weight, k_weight, ref):
-    """(phases pointer, rot) after the checks shared by the calls below."""
-    torch = _torch()
+    """rot, after the checks shared by the calls below."""
+    d = ref.shape[-1]
+    rot = 0
     if phases is not None:
-        _need(phases.dtype == torch.int64 and phases.dim() == 1, "phases must be 1-D int64 (rope_phases)")
-        _need(2 * phases.numel() <= ref.shape[-1], "more rotation pairs than half of the head")
-        _contig(phases)
-    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _like(w, ref, (ref.shape[-1],), n)
-            _contig(w)
-    return _p(phases), 0 if phases is None else 2 * phases.numel()
-
-
-def _bshd(t):
-    """(b, s, h, d) sizes of a tensor, or zeros where there is none."""
-    _need(t is None or t.dim() == 4, "q and k must be (b, s, heads, d)")
-    return (0, 0, 0, 0) if t is None else tuple(t.shape)
+        rot = 2 * phases.numel()
+        if phases.dtype != _torch().int64 or phases.dim() != 1:
+            raise ValueError("phases must be 1-D int64 (rope_phases)")
+        if rot > d:
+            raise ValueError("more rotation pairs than half of the head")
+    if q_weight is not None:
+        _like(q_weight, ref, (d,), "q_weight")
+    if k_weight is not None:
+        _like(k_weight, ref, (d,), "k_weight")
+    _contig(phases, q_weight, k_weight)
+    return rot
 
 
 def _qk_sizes(q, k):
-    ref = q if q is not None else k
-    _need(ref is not None, "q or k is needed")
-    b, s, _, d = _bshd(ref)
-    for t in (q, k):
-        if t is not None:
-            _need(t.dtype == ref.dtype and _bshd(t)[:2] == (b, s) and t.shape[3] == d,
-                  "q and k must share batch, length, d and dtype")
-    return ref, b, s, _bshd(q)[2], _bshd(k)[2], d
+    """(q or k, b, s, hq, hkv, d); either of the two may be None."""
+    ref = k if q is None else q
+    if ref is None:
+        raise ValueError("q or k is needed")
+    if ref.dim() != 4:
+        raise ValueError("q and k must be (b, s, heads, d)")
+    b, s, h, d = ref.shape
+    if q is None:
+        return ref, b, s, 0, h, d
+    if k is None:
+        return ref, b, s, h, 0, d
+    if k.dtype != q.dtype or k.shape != (b, s, k.shape[-2], d):
+        raise ValueError("q and k must share batch, length, d and dtype")
+    return ref, b, s, h, k.shape[2], d
 
 
 def _positions(positions, b, s):
-    if positions is not None:
-        _need(positions.dtype == _torch().int32 and positions.numel() == b * s,
-              "positions must be int32 with one entry per token")
-        _contig(positions)
-    return _p(positions)
+    if positions is None:
+        return None
+    if positions.dtype != _torch().int32 or positions.numel() != b * s:
+        raise ValueError("positions must be int32 with one entry per token")
+    _contig(positions)
+    return positions.data_ptr()
+
+
+def _result(t, like, what):
+    """The output `t`, or a new contiguous one; None where there is no input."""
+    if like is None:
+        return None
+    if t is None:
+        torch = _torch()
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
+    _like(t, like, like.shape, what)
+    return t
 
 
 def qk_norm_rope(q, k, *, phases=None, positions=None, interleaved=False, q_weight=None,
@@ -595,22 +640,15 @@ def qk_norm_rope(q, k, *, phases=None, positions=None, interleaved=False, q_weig
     phases are, see rope_phases) of q (b,s,hq,d) and k (b,s,hkv,d) in one pass;
     either may be None, token-strided views are taken, and q_out=q / k_out=k
     works in place.  positions: int32 (b,s), default 0..s-1."""
-    torch = _torch()
     ref, b, s, hq, hkv, d = _qk_sizes(q, k)
-    cf = torch.contiguous_format
-    if q is not None:
-        q_out = torch.empty_like(q, memory_format=cf) if q_out is None else q_out
-        _like(q_out, ref, q.shape, "q_out")
-    if k is not None:
-        k_out = torch.empty_like(k, memory_format=cf) if k_out is None else k_out
-        _like(k_out, ref, k.shape, "k_out")
-    ph, rot = _rope_args(phases, q_weight, k_weight, ref)
-    rs = [_row_stride(t) for t in (q, k, q_out, k_out)]
+    rot = _rope_args(phases, q_weight, k_weight, ref)
+    q_out, k_out = _result(q_out, q, "q_out"), _result(k_out, k, "k_out")
     with _on_device(q, k, q_out, k_out, phases, positions, q_weight, k_weight):
-        st = lib().attn_qk_norm_rope(_p(q), _p(k), _p(q_out), _p(k_out), *rs, _p(q_weight),
-                                     _p(k_weight), float(eps), ph, rot, int(bool(interleaved)),
-                                     _positions(positions, b, s), _dt(ref), b, s, hq, hkv, d,
-                                     _stream())
+        st = lib().attn_qk_norm_rope(_p(q), _p(k), _p(q_out), _p(k_out), _row_stride(q),
+                                     _row_stride(k), _row_stride(q_out), _row_stride(k_out),
+                                     _p(q_weight), _p(k_weight), eps, _p(phases), rot,
+                                     1 if interleaved else 0, _positions(positions, b, s),
+                                     _dt(ref), b, s, hq, hkv, d, _stream())
     _check(st, "attn_qk_norm_rope")
     return q_out, k_out
 
@@ -630,38 +668,29 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, *, phases=None, positions=None, inter
     """Backward of qk_norm_rope -> dq, dk, dq_weight, dk_weight (None where the
     forward had none).  dq / dk may be views of a packed gradient, or dq_out /
     dk_out themselves."""
-    torch = _torch()
     ref, b, s, hq, hkv, d = _qk_sizes(q, k)
-    _need((dq_out is None) == (q is None) and (dk_out is None) == (k is None),
-          "the gradients must be those of the forward's outputs")
-    cf = torch.contiguous_format
-    for t, g, n in ((q, dq_out, "dq_out"), (k, dk_out, "dk_out")):
-        if t is not None:
-            _like(g, ref, t.shape, n)
+    rot = _rope_args(phases, q_weight, k_weight, ref)
+    if (dq_out is None) != (q is None) or (dk_out is None) != (k is None):
+        raise ValueError("the gradients must be those of the forward's outputs")
     if q is not None:
-        dq = torch.empty_like(q, memory_format=cf) if dq is None else dq
-        _like(dq, ref, q.shape, "dq")
+        _like(dq_out, q, q.shape, "dq_out")
     if k is not None:
-        dk = torch.empty_like(k, memory_format=cf) if dk is None else dk
-        _like(dk, ref, k.shape, "dk")
-    if q is not None and q_weight is not None and dq_weight is None:
-        dq_weight = torch.empty_like(q_weight)
-    if k is not None and k_weight is not None and dk_weight is None:
-        dk_weight = torch.empty_like(k_weight)
-    for w, n in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
-        if w is not None:
-            _like(w, ref, (d,), n)
-    ws = qk_norm_rope_bwd_workspace(q, k) if workspace is None else workspace
-    ph, rot = _rope_args(phases, q_weight, k_weight, ref)
-    _contig(dq_out, dk_out, dq_weight, dk_weight, ws)
-    rs = [_row_stride(t) for t in (q, k, dq, dk)]
+        _like(dk_out, k, k.shape, "dk_out")
+    dq, dk = _result(dq, q, "dq"), _result(dk, k, "dk")
+    dq_weight = _result(dq_weight, None if q is None else q_weight, "dq_weight")
+    dk_weight = _result(dk_weight, None if k is None else k_weight, "dk_weight")
+    if workspace is None:
+        workspace = qk_norm_rope_bwd_workspace(q, k)
+    _contig(dq_out, dk_out, dq_weight, dk_weight, workspace)
     with _on_device(q, k, dq_out, dk_out, dq, dk, phases, positions, q_weight, k_weight, dq_weight,
-                    dk_weight, ws):
-        st = lib().attn_qk_norm_rope_bwd(_p(q), _p(k), _p(dq_out), _p(dk_out), _p(dq), _p(dk), *rs,
-                                         _p(q_weight), _p(k_weight), _p(dq_weight), _p(dk_weight),
-                                         float(eps), ph, rot, int(bool(interleaved)),
-                                         _positions(positions, b, s), _dt(ref), b, s, hq, hkv, d,
-                                         _p(ws), ws.numel() * ws.element_size(), _stream())
+                    dk_weight, workspace):
+        st = lib().attn_qk_norm_rope_bwd(_p(q), _p(k), _p(dq_out), _p(dk_out), _p(dq), _p(dk),
+                                         _row_stride(q), _row_stride(k), _row_stride(dq),
+                                         _row_stride(dk), _p(q_weight), _p(k_weight),
+                                         _p(dq_weight), _p(dk_weight), eps, _p(phases), rot,
+                                         1 if interleaved else 0, _positions(positions, b, s),
+                                         _dt(ref), b, s, hq, hkv, d, _p(workspace),
+                                         workspace.nbytes, _stream())
     _check(st, "attn_qk_norm_rope_bwd")
     return dq, dk, dq_weight, dk_weight
 
@@ -673,30 +702,30 @@ def kvcache_append(k_new, v_new, k_cache, v_cache, cu_seqlens, cache_seqlens, *,
     the positions behind cache_seqlens, with the norm and rotation of the keys
     on the way; q (T,hq,d), if given, is normed and rotated at the same
     positions into q_out, which is returned.  Does not modify cache_seqlens."""
-    torch = _torch()
     total, hkv, d = k_new.shape
     batch, num_pages, page_size, max_pages = _cache_args(k_cache, v_cache, cu_seqlens,
                                                          cache_seqlens, block_table)
     _like(v_new, k_new, k_new.shape, "v_new")
-    _need(k_cache.dtype == k_new.dtype and tuple(k_cache.shape[2:]) == (hkv, d),
-          "the cache must have the heads, d and dtype of the new keys")
+    if k_cache.dtype != k_new.dtype or k_cache.shape[2] != hkv or k_cache.shape[3] != d:
+        raise ValueError("the cache must have the heads, d and dtype of the new keys")
     hq = 0
-    if q is not None:
+    if q is None:
+        q_out = None
+    else:
         hq = q.shape[1]
         _like(q, k_new, (total, hq, d), "q")
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format) if q_out is None else q_out
-        _like(q_out, q, q.shape, "q_out")
+        q_out = _result(q_out, q, "q_out")
         _contig(q_out)
-    ph, rot = _rope_args(phases, q_weight, k_weight, k_new)
-    rs = [_packed_stride(t) for t in (q, k_new, v_new)]
+    rot = _rope_args(phases, q_weight, k_weight, k_new)
     with _on_device(k_new, v_new, k_cache, v_cache, cu_seqlens, cache_seqlens, block_table, q,
                     q_out, phases, q_weight, k_weight):
-        st = lib().attn_kvcache_append(_p(q), _p(q_out) if q is not None else None, _p(k_new),
-                                       _p(v_new), *rs, _p(k_cache), _p(v_cache),
-                                       _page_stride(k_cache), _page_stride(v_cache),
+        st = lib().attn_kvcache_append(_p(q), _p(q_out), _p(k_new), _p(v_new), _packed_stride(q),
+                                       _packed_stride(k_new), _packed_stride(v_new), _p(k_cache),
+                                       _p(v_cache), _page_stride(k_cache), _page_stride(v_cache),
                                        _p(cu_seqlens), _p(cache_seqlens), _p(block_table),
                                        num_pages, page_size, max_pages, _p(q_weight),
-                                       _p(k_weight), float(eps), ph, rot, int(bool(interleaved)),
-                                       _dt(k_new), batch, total, hq, hkv, d, _stream())
+                                       _p(k_weight), eps, _p(phases), rot,
+                                       1 if interleaved else 0, _dt(k_new), batch, total, hq, hkv,
+                                       d, _stream())
     _check(st, "attn_kvcache_append")
-    return q_out if q is not None else None
+    return q_out
