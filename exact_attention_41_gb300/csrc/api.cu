@@ -654,7 +654,7 @@ attn_status attn_qk_norm_rope(const void *q, const void *k, void *q_out, void *k
 size_t attn_qk_norm_rope_bwd_workspace_size(int b, int s, int hq, int hkv, int d) {
   if (b <= 0 || s <= 0 || hq + hkv <= 0 || d <= 0) return 0;
   const DeviceInfo *di = device_info();
-  return align256(sizeof(float) * 2 * (size_t)d * rope_bwd_blocks(di ? di->sms : 152));
+  return align256(sizeof(float) * (size_t)d * rope_bwd_blocks(di ? di->sms : 152));
 }
 
 attn_status attn_qk_norm_rope_bwd(const void *q, const void *k, const void *dq_out,

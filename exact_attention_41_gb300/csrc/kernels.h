@@ -119,7 +119,7 @@ struct RopeArgs {
   int64_t q_rs, k_rs, v_rs, q_out_rs, k_out_rs, v_out_rs, gq_rs, gk_rs;
   const void *q_weight, *k_weight;  // nullptr: no norm
   void *q_gw, *k_gw;                // backward: gradients of the weights
-  float *gw_part;                   // backward: workspace (blocks, 2, d) fp32
+  float *gw_part;                   // backward: workspace (blocks, d) fp32
   float eps;
   const uint64_t *phases;       // (rot / 2) turns per position in 2^-64 turns
   int rot, interleaved;
@@ -210,7 +210,7 @@ cudaError_t launch_paged_tc(const PagedArgs &a, const PagedPlan &plan, cudaStrea
 // Forward of the norm and rotation, or the append when a.cu_seqlens is set.
 cudaError_t launch_norm_rope(const RopeArgs &a, int sms, cudaStream_t st);
 cudaError_t launch_norm_rope_bwd(const RopeArgs &a, int sms, cudaStream_t st);
-// Most blocks of the backward, each of which writes 2 * d floats of workspace.
+// Most blocks of the backward, each of which writes d floats of workspace.
 int rope_bwd_blocks(int sms);
 // cache_seqlens[i] += s_new for i < b.
 cudaError_t launch_kvcache_advance(int32_t *cache_seqlens, int b, int s_new, cudaStream_t st);

@@ -21,6 +21,8 @@
 // cosines and sines are then the same for every head of the token, and a head
 // is D / 16 neighbouring lanes, so the norm's sum is log2(D / 16) shuffles.
 // Everything is held in fp32 and rounded once, to the output.
+#include <algorithm>
+
 #include "kernels.h"
 
 namespace attn {
@@ -28,6 +30,7 @@ namespace {
 
 constexpr int kWarps = 4;       // warps of a forward or append block
 constexpr int kBwdWarps = 8;    // warps of a backward block
+constexpr int kBwdBlocks = 2;   // its blocks on one SM
 
 // Where the 16 elements of thread `t` of a head sit: elements 0-7 at o0, 8-15
 // at o1.
@@ -41,10 +44,25 @@ __device__ __forceinline__ Slots slots_of(int t, int rot, int interleaved) {
   return {16 * t, 16 * t + 8, turn};
 }
 
+// A thread's 16 elements of a head as loaded, so that the next head's can be
+// on their way while this one's are worked on.
+struct Raw {
+  uint4 a, b;
+};
 template <typename T>
-__device__ __forceinline__ void load16(const T *row, const Slots &sl, float (&x)[16]) {
-  load_vec<T, 8>(row + sl.o0, x);
-  load_vec<T, 8>(row + sl.o1, x + 8);
+__device__ __forceinline__ Raw load_raw(const T *row, const Slots &sl, bool on) {
+  if (!on) return {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  return {*reinterpret_cast<const uint4 *>(row + sl.o0), *reinterpret_cast<const uint4 *>(row + sl.o1)};
+}
+template <typename T>
+__device__ __forceinline__ void widen(const Raw &r, float (&x)[16]) {
+  const uint32_t u[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float2 f = Elem<T>::to_f2(u[e]);
+    x[2 * e] = f.x;
+    x[2 * e + 1] = f.y;
+  }
 }
 template <typename T>
 __device__ __forceinline__ void store16(T *row, const Slots &sl, const float (&x)[16]) {
@@ -63,8 +81,11 @@ __device__ __forceinline__ void angles(const uint64_t *phases, int t, int64_t po
     for (int u = 0; u < 2; ++u) {
       // turns mod 1 in 2^-64, rounded to 2^-32 of a turn = 2^-31 of a half turn
       const uint64_t turn = (uint64_t)pos * (u ? f.y : f.x) + 0x80000000ull;
-      const float half_turns = (float)(int32_t)(turn >> 32) * 4.656612873077393e-10f;  // 2^-31
-      sincospif(half_turns, &s[2 * e + u], &c[2 * e + u]);
+      // the hardware's sine and cosine: within 2^-21 on [-pi, pi], a thousandth
+      // of fp16's half step at 1
+      const float a = (float)(int32_t)(turn >> 32) * 1.4629180792671596e-9f;  // pi 2^-31
+      s[2 * e + u] = __sinf(a);
+      c[2 * e + u] = __cosf(a);
     }
   }
 }
@@ -182,34 +203,40 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const RopeArgs a
   if (sl.turn) angles(a.phases, t, pos, c, s);
   const int nq = (a.hq + HPW - 1) / HPW, nk = (a.hkv + HPW - 1) / HPW;
   const int n = nq + nk * (kAppend ? 2 : 1);
+  // group it: heads HPW it' .. of the queries, keys or values (kind 0, 1, 2)
+  const auto kind_of = [&](int it) { return it < nq ? 0 : it < nq + nk ? 1 : 2; };
+  const auto head_of = [&](int it) {
+    return (it < nq ? it : it < nq + nk ? it - nq : it - nq - nk) * HPW + sub;
+  };
+  const auto load = [&](int it) {
+    if (it >= n) return Raw{};
+    const int k = kind_of(it), h = head_of(it);
+    const T *src = k == 0 ? qs : k == 1 ? ks : static_cast<const T *>(a.v) + row * a.v_rs;
+    return load_raw(src + h * D, k == 2 ? Slots{16 * t, 16 * t + 8, false} : sl,
+                    h < (k == 0 ? a.hq : a.hkv));
+  };
+  Raw next = load(part);
   for (int it = part; it < n; it += a.parts) {
-    if (kAppend && it >= nq + nk) {  // values: copied
-      const int h = (it - nq - nk) * HPW + sub;
-      if (h < a.hkv && vd) {
-        const T *src = static_cast<const T *>(a.v) + row * a.v_rs + h * D + 16 * t;
+    const Raw now = next;
+    next = load(it + a.parts);
+    const int k = kind_of(it), h = head_of(it);
+    const bool on = h < (k == 0 ? a.hq : a.hkv);
+    if (k == 2) {  // values: copied
+      if (on && vd) {
         uint4 *dst = reinterpret_cast<uint4 *>(vd + h * D + 16 * t);
-        dst[0] = reinterpret_cast<const uint4 *>(src)[0];
-        dst[1] = reinterpret_cast<const uint4 *>(src)[1];
+        dst[0] = now.a;
+        dst[1] = now.b;
       }
       continue;
     }
-    const bool is_q = it < nq;
-    const int h = (is_q ? it : it - nq) * HPW + sub;
-    const bool on = h < (is_q ? a.hq : a.hkv);
-    const T *src = (is_q ? qs : ks) + h * D;
-    T *dst = is_q ? qd : kd;
-    const T *w = static_cast<const T *>(is_q ? a.q_weight : a.k_weight);
+    T *dst = k == 0 ? qd : kd;
+    const T *w = static_cast<const T *>(k == 0 ? a.q_weight : a.k_weight);
     float x[16];
-    if (on) {
-      load16(src, sl, x);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = 0.f;
-    }
+    widen<T>(now, x);
     if (w) {
       const float r = inv_rms<D>(x, a.eps);
       float wv[16];
-      load16(w, sl, wv);
+      widen<T>(load_raw(w, sl, true), wv);
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[e] = x[e] * r * wv[e];
     }
@@ -218,112 +245,130 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const RopeArgs a
   }
 }
 
-// Gradient of one head's norm and rotation; adds the weight's gradient.
-template <typename T, int D>
-__device__ __forceinline__ void bwd_head(const T *x_row, const T *gy_row, T *gx_row, bool on,
-                                         const T *w, float eps, const Slots &sl,
-                                         const float (&c)[8], const float (&s)[8],
-                                         int interleaved, float (&gw)[16]) {
-  float g[16], x[16];
-#pragma unroll
-  for (int e = 0; e < 16; ++e) g[e] = x[e] = 0.f;
-  if (on) {
-    load16(gy_row, sl, g);
-    if (w) load16(x_row, sl, x);
-  }
-  if (sl.turn) rotate(g, c, s, -1.f, interleaved);
-  if (w) {
-    float wv[16];
-    load16(w, sl, wv);
-    const float r = inv_rms<D>(x, eps);
-    float dot = 0.f;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      x[e] *= r;
-      gw[e] = fmaf(g[e], x[e], gw[e]);
-      g[e] *= wv[e];
-      dot = fmaf(g[e], x[e], dot);
-    }
-    dot = head_sum<D>(dot) * (1.f / D);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) g[e] = (g[e] - x[e] * dot) * r;
-  }
-  if (on) store16(gx_row, sl, g);
-}
-
-// Persistent: a warp takes every (blocks * kBwdWarps)-th token and keeps the
-// weights' gradients of its tokens in registers; the block adds its warps in
-// order and writes one partial per weight, which a second kernel adds in
-// order, so the result does not change from run to run.
-template <typename T, int D>
-__global__ void __launch_bounds__(kBwdWarps * 32) norm_rope_bwd_kernel(const RopeArgs a) {
+// Gradient.  Persistent: blocks 0 .. blocks_q - 1 take the queries, the others
+// the keys (each kind then needs one weight and one set of sums in registers),
+// a warp every (blocks * kBwdWarps)-th token, HPW heads at a time, with the next
+// heads' rows loaded ahead.  The sums of the weight's gradient stay in
+// registers; a block adds its warps in order and writes one partial, which a
+// second kernel adds in order, so the result does not change from run to run.
+template <typename T, int D, bool kNorm>
+__device__ __forceinline__ void bwd_kind(const RopeArgs &a, const T *x, const T *gy, T *gx,
+                                         int64_t x_rs, int64_t gy_rs, int64_t gx_rs, int heads,
+                                         const T *w, int block, int blocks, float *gw_out) {
   constexpr int LPH = D / 16, HPW = 32 / LPH;
-  __shared__ float part[kBwdWarps][2][D];
+  __shared__ float part[kBwdWarps][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane % LPH, sub = lane / LPH;
   const Slots sl = slots_of(t, a.rot, a.interleaved);
-  float gwq[16], gwk[16];
+  const int stride = blocks * kBwdWarps;
+  float gw[16];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) gwq[e] = gwk[e] = 0.f;
-  for (int64_t row = (int64_t)blockIdx.x * kBwdWarps + warp; row < a.rows;
-       row += (int64_t)gridDim.x * kBwdWarps) {
-    const int64_t pos = a.positions ? a.positions[row] : row % a.s;
-    float c[8], s[8];
-    if (sl.turn) angles(a.phases, t, pos, c, s);
-    for (int h = sub; h - sub < a.hq; h += HPW)
-      bwd_head<T, D>(static_cast<const T *>(a.q) + row * a.q_rs + h * D,
-                     static_cast<const T *>(a.gq) + row * a.gq_rs + h * D,
-                     static_cast<T *>(a.q_out) + row * a.q_out_rs + h * D, h < a.hq,
-                     static_cast<const T *>(a.q_weight), a.eps, sl, c, s, a.interleaved, gwq);
-    for (int h = sub; h - sub < a.hkv; h += HPW)
-      bwd_head<T, D>(static_cast<const T *>(a.k) + row * a.k_rs + h * D,
-                     static_cast<const T *>(a.gk) + row * a.gk_rs + h * D,
-                     static_cast<T *>(a.k_out) + row * a.k_out_rs + h * D, h < a.hkv,
-                     static_cast<const T *>(a.k_weight), a.eps, sl, c, s, a.interleaved, gwk);
-  }
-  if (!a.q_weight && !a.k_weight) return;
-  // the HPW heads of a warp, then its warps
-#pragma unroll
-  for (int e = 0; e < 16; ++e) {
-#pragma unroll
-    for (int o = LPH; o < 32; o <<= 1) {
-      gwq[e] += __shfl_xor_sync(0xffffffffu, gwq[e], o);
-      gwk[e] += __shfl_xor_sync(0xffffffffu, gwk[e], o);
+  for (int e = 0; e < 16; ++e) gw[e] = 0.f;
+  Raw wr{};
+  if constexpr (kNorm) wr = load_raw(w, sl, true);
+  int64_t row = (int64_t)block * kBwdWarps + warp;
+  int h = sub;
+  Raw g_next = load_raw(gy + row * gy_rs + h * D, sl, row < a.rows && h < heads), x_next{};
+  if constexpr (kNorm) x_next = load_raw(x + row * x_rs + h * D, sl, row < a.rows && h < heads);
+  float c[8], s[8];
+  while (row < a.rows) {
+    if (h == sub && sl.turn) angles(a.phases, t, a.positions ? a.positions[row] : row % a.s, c, s);
+    const Raw g_now = g_next, x_now = x_next;
+    const int64_t r0 = row;
+    const int h0 = h;
+    h += HPW;
+    if (h - sub >= heads) {
+      h = sub;
+      row += stride;
     }
-  }
-  if (sub == 0) {
+    const bool more = row < a.rows && h < heads;
+    g_next = load_raw(gy + row * gy_rs + h * D, sl, more);
+    if constexpr (kNorm) x_next = load_raw(x + row * x_rs + h * D, sl, more);
+    float g[16];
+    widen<T>(g_now, g);
+    if (sl.turn) rotate(g, c, s, -1.f, a.interleaved);
+    if constexpr (kNorm) {
+      float xh[16], wv[16];
+      widen<T>(x_now, xh);
+      widen<T>(wr, wv);
+      const float r = inv_rms<D>(xh, a.eps);
+      float dot = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      part[warp][0][sl.o0 + e] = gwq[e];
-      part[warp][0][sl.o1 + e] = gwq[8 + e];
-      part[warp][1][sl.o0 + e] = gwk[e];
-      part[warp][1][sl.o1 + e] = gwk[8 + e];
+      for (int e = 0; e < 16; ++e) {
+        xh[e] *= r;
+        gw[e] = fmaf(g[e], xh[e], gw[e]);
+        g[e] *= wv[e];
+        dot = fmaf(g[e], xh[e], dot);
+      }
+      dot = head_sum<D>(dot) * (-1.f / D);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) g[e] = fmaf(xh[e], dot, g[e]) * r;
     }
+    if (h0 < heads) store16(gx + r0 * gx_rs + h0 * D, sl, g);
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 2 * D; i += kBwdWarps * 32) {
-    float v = 0.f;
+  if constexpr (kNorm) {
+    // the HPW heads of a warp, then its warps
 #pragma unroll
-    for (int w = 0; w < kBwdWarps; ++w) v += part[w][i / D][i % D];
-    a.gw_part[(int64_t)blockIdx.x * 2 * D + i] = v;
+    for (int e = 0; e < 16; ++e) {
+#pragma unroll
+      for (int o = LPH; o < 32; o <<= 1) gw[e] += __shfl_xor_sync(0xffffffffu, gw[e], o);
+    }
+    if (sub == 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        part[warp][sl.o0 + e] = gw[e];
+        part[warp][sl.o1 + e] = gw[8 + e];
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < D; i += kBwdWarps * 32) {
+      float v = 0.f;
+#pragma unroll
+      for (int u = 0; u < kBwdWarps; ++u) v += part[u][i];
+      gw_out[i] = v;
+    }
   }
 }
 
-// gw = sum of the blocks' partials, in a fixed order; 32 columns a block.
 template <typename T, int D>
-__global__ void __launch_bounds__(1024) weight_grad_kernel(const RopeArgs a, int blocks) {
+__global__ void __launch_bounds__(kBwdWarps * 32, kBwdBlocks)
+    norm_rope_bwd_kernel(const RopeArgs a, const int blocks_q) {
+  const int b = blockIdx.x;
+  const bool is_q = b < blocks_q;
+  const T *x = static_cast<const T *>(is_q ? a.q : a.k);
+  const T *gy = static_cast<const T *>(is_q ? a.gq : a.gk);
+  T *gx = static_cast<T *>(is_q ? a.q_out : a.k_out);
+  const int64_t x_rs = is_q ? a.q_rs : a.k_rs, gy_rs = is_q ? a.gq_rs : a.gk_rs;
+  const int64_t gx_rs = is_q ? a.q_out_rs : a.k_out_rs;
+  const T *w = static_cast<const T *>(is_q ? a.q_weight : a.k_weight);
+  const int heads = is_q ? a.hq : a.hkv;
+  const int block = is_q ? b : b - blocks_q, blocks = is_q ? blocks_q : gridDim.x - blocks_q;
+  if (w)
+    bwd_kind<T, D, true>(a, x, gy, gx, x_rs, gy_rs, gx_rs, heads, w, block, blocks,
+                         a.gw_part + (int64_t)b * D);
+  else
+    bwd_kind<T, D, false>(a, x, gy, gx, x_rs, gy_rs, gx_rs, heads, w, block, blocks, nullptr);
+}
+
+// gw = sum of the blocks' partials, in a fixed order; 32 columns a block, the
+// queries' weight first.
+template <typename T, int D>
+__global__ void __launch_bounds__(1024) weight_grad_kernel(const RopeArgs a, int blocks_q, int blocks) {
   __shared__ float sum[32][33];
   const int col = threadIdx.x & 31, grp = threadIdx.x >> 5;
-  const int i = blockIdx.x * 32 + col;
+  const bool is_q = blockIdx.x < D / 32;
+  T *dst = static_cast<T *>(is_q ? a.q_gw : a.k_gw);
+  if (!dst) return;
+  const int i = blockIdx.x % (D / 32) * 32 + col;
   float v = 0.f;
-  for (int b = grp; b < blocks; b += 32) v += a.gw_part[(int64_t)b * 2 * D + i];
+  for (int b = (is_q ? 0 : blocks_q) + grp; b < (is_q ? blocks_q : blocks); b += 32)
+    v += a.gw_part[(int64_t)b * D + i];
   sum[grp][col] = v;
   __syncthreads();
   if (grp == 0) {
     float r = 0.f;
 #pragma unroll
     for (int g = 0; g < 32; ++g) r += sum[g][col];
-    T *dst = static_cast<T *>(i < D ? a.q_gw : a.k_gw);
-    if (dst) dst[i % D] = Elem<T>::from_f(r);
+    dst[i] = Elem<T>::from_f(r);
   }
 }
 
@@ -351,15 +396,21 @@ cudaError_t fwd(RopeArgs a, int sms, cudaStream_t st) {
 
 template <typename T, int D>
 cudaError_t bwd(const RopeArgs &a, int sms, cudaStream_t st) {
+  // blocks for queries and keys by their heads; no more than there are tokens for
   const int64_t want = ((int64_t)a.rows + kBwdWarps - 1) / kBwdWarps;
-  const int blocks = (int)(want < rope_bwd_blocks(sms) ? want : rope_bwd_blocks(sms));
-  debug_log("norm+rotation backward: norm_rope_bwd_kernel d=%d, %d tokens, grid=%d", D, a.rows, blocks);
+  const int most = rope_bwd_blocks(sms), heads = a.hq + a.hkv;
+  const auto share = [&](int h) {
+    return h == 0 ? 0 : (int)std::min<int64_t>(want, std::max(1, (int)((int64_t)most * h / heads)));
+  };
+  const int blocks_q = share(a.hq), blocks = blocks_q + share(a.hkv);
+  debug_log("norm+rotation backward: norm_rope_bwd_kernel d=%d, %d tokens, grid=%d (%d for queries)",
+            D, a.rows, blocks, blocks_q);
   if (blocks > 0) {  // no tokens: the weights' gradients are empty sums
-    norm_rope_bwd_kernel<T, D><<<blocks, kBwdWarps * 32, 0, st>>>(a);
+    norm_rope_bwd_kernel<T, D><<<blocks, kBwdWarps * 32, 0, st>>>(a, blocks_q);
     count_launches(1);
   }
   if (a.q_weight || a.k_weight) {
-    weight_grad_kernel<T, D><<<2 * D / 32, 1024, 0, st>>>(a, blocks);
+    weight_grad_kernel<T, D><<<2 * D / 32, 1024, 0, st>>>(a, blocks_q, blocks);
     count_launches(1);
   }
   return cudaGetLastError();
@@ -367,7 +418,8 @@ cudaError_t bwd(const RopeArgs &a, int sms, cudaStream_t st) {
 
 }  // namespace
 
-int rope_bwd_blocks(int sms) { return 3 * sms; }
+// (at least one block each for queries and keys)
+int rope_bwd_blocks(int sms) { return std::max(2, kBwdBlocks * sms); }
 
 cudaError_t launch_norm_rope(const RopeArgs &a, int sms, cudaStream_t st) {
   const bool bf = a.dtype == ATTN_BF16;

@@ -3,10 +3,11 @@ to a paged cache, against the float64 oracle.
 
 Tolerances, from the arithmetic (h: half a step of the storage type, relative;
 u = 2^-24):
-* the angle is exact to 2^-32 turns, its fp32 value to pi u, sincospi to 2 u, so
-  a turned pair (a, b) is off by at most 10 u (|a| + |b|); the norm (16 adds a
-  thread, 4 across lanes, one reciprocal root, two products) adds 26 u |z|;
-  together below 64 u times the largest |z| of the head = Z.  |y| rounds by
+* the angle is exact to 2^-32 turns, its fp32 value to pi u, the hardware's sine
+  and cosine to 2^-21 = 8 u, so a turned pair (a, b) is off by at most 14 u
+  (|a| + |b|) with its products and sum; the norm (16 adds a thread, 4 across
+  lanes, one reciprocal root, two products) adds 26 u |z|; together below 64 u
+  times the largest |z| of the head = Z.  |y| rounds by
   h |y|:  |dy| <= h |y| + 64 u Z.
 * gradient: gz as above from gy (64 u G), then gx = r (gz w - xh mean(gz w xh));
   every factor carries at most 32 u more, so |dgx| <= h |gx| + 128 u r W G (1 + X)
