@@ -24,6 +24,7 @@
 #include <algorithm>
 
 #include "kernels.h"
+#include "sm103.cuh"
 
 namespace attn {
 namespace {
@@ -31,6 +32,8 @@ namespace {
 constexpr int kWarps = 4;       // warps of a forward or append block
 constexpr int kBwdWarps = 8;    // warps of a backward block
 constexpr int kBwdBlocks = 2;   // its blocks on one SM
+constexpr int kBwdStages = 4;   // heads in flight per thread: 3 ahead of the one in hand
+constexpr int kBwdSmem = kBwdStages * 4 * kBwdWarps * 32 * 16;
 
 // Where the 16 elements of thread `t` of a head sit: elements 0-7 at o0, 8-15
 // at o1.
@@ -247,14 +250,17 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const RopeArgs a
 
 // Gradient.  Persistent: blocks 0 .. blocks_q - 1 take the queries, the others
 // the keys (each kind then needs one weight and one set of sums in registers),
-// a warp every (blocks * kBwdWarps)-th token, HPW heads at a time, with the next
-// heads' rows loaded ahead.  The sums of the weight's gradient stay in
+// a warp every (blocks * kBwdWarps)-th token, HPW heads at a time.  Each thread
+// copies its own pieces of the next three head groups into shared memory
+// (cp.async: bytes in flight without registers; 98 KB a SM, where the loads in
+// registers that this replaced held a third of that).  The sums of the weight's gradient stay in
 // registers; a block adds its warps in order and writes one partial, which a
 // second kernel adds in order, so the result does not change from run to run.
 template <typename T, int D, bool kNorm>
 __device__ __forceinline__ void bwd_kind(const RopeArgs &a, const T *x, const T *gy, T *gx,
                                          int64_t x_rs, int64_t gy_rs, int64_t gx_rs, int heads,
-                                         const T *w, int block, int blocks, float *gw_out) {
+                                         const T *w, int block, int blocks, float *gw_out,
+                                         uint8_t *ring_smem) {
   constexpr int LPH = D / 16, HPW = 32 / LPH;
   __shared__ float part[kBwdWarps][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane % LPH, sub = lane / LPH;
@@ -265,14 +271,44 @@ __device__ __forceinline__ void bwd_kind(const RopeArgs &a, const T *x, const T 
   for (int e = 0; e < 16; ++e) gw[e] = 0.f;
   Raw wr{};
   if constexpr (kNorm) wr = load_raw(w, sl, true);
-  int64_t row = (int64_t)block * kBwdWarps + warp;
-  int h = sub;
-  Raw g_next = load_raw(gy + row * gy_rs + h * D, sl, row < a.rows && h < heads), x_next{};
-  if constexpr (kNorm) x_next = load_raw(x + row * x_rs + h * D, sl, row < a.rows && h < heads);
+  // pieces of this thread: [stage][gy a, gy b, x a, x b][thread]
+  uint4 *ring = reinterpret_cast<uint4 *>(ring_smem) + threadIdx.x;
+  constexpr int kThreads = kBwdWarps * 32;
+  int64_t row = (int64_t)block * kBwdWarps + warp, row_in = row;  // in hand; next to copy
+  int h = sub, h_in = sub;
+  const auto copy = [&](int stage) {
+    if (row_in < a.rows) {
+      const uint32_t n = h_in < heads ? 16 : 0;
+      const int64_t at = n ? h_in * D : 0;
+      uint4 *dst = ring + stage * 4 * kThreads;
+      const T *src = gy + row_in * gy_rs + at;
+      sm103::cp_async_16(dst, src + sl.o0, n);
+      sm103::cp_async_16(dst + kThreads, src + sl.o1, n);
+      if constexpr (kNorm) {
+        const T *xs = x + row_in * x_rs + at;
+        sm103::cp_async_16(dst + 2 * kThreads, xs + sl.o0, n);
+        sm103::cp_async_16(dst + 3 * kThreads, xs + sl.o1, n);
+      }
+      h_in += HPW;
+      if (h_in - sub >= heads) {
+        h_in = sub;
+        row_in += stride;
+      }
+    }
+    sm103::cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kBwdStages - 1; ++i) copy(i);
   float c[8], s[8];
-  while (row < a.rows) {
+  for (int stage = 0; row < a.rows; stage = (stage + 1) % kBwdStages) {
     if (h == sub && sl.turn) angles(a.phases, t, a.positions ? a.positions[row] : row % a.s, c, s);
-    const Raw g_now = g_next, x_now = x_next;
+    sm103::cp_async_wait<kBwdStages - 2>();
+    const uint4 *src = ring + stage * 4 * kThreads;
+    const Raw g_now{src[0], src[kThreads]};
+    Raw x_now{};
+    if constexpr (kNorm) x_now = {src[2 * kThreads], src[3 * kThreads]};
+    // (into the stage that the previous turn has used up)
+    copy((stage + kBwdStages - 1) % kBwdStages);
     const int64_t r0 = row;
     const int h0 = h;
     h += HPW;
@@ -280,9 +316,6 @@ __device__ __forceinline__ void bwd_kind(const RopeArgs &a, const T *x, const T 
       h = sub;
       row += stride;
     }
-    const bool more = row < a.rows && h < heads;
-    g_next = load_raw(gy + row * gy_rs + h * D, sl, more);
-    if constexpr (kNorm) x_next = load_raw(x + row * x_rs + h * D, sl, more);
     float g[16];
     widen<T>(g_now, g);
     if (sl.turn) rotate(g, c, s, -1.f, a.interleaved);
@@ -332,8 +365,11 @@ __device__ __forceinline__ void bwd_kind(const RopeArgs &a, const T *x, const T 
 template <typename T, int D>
 __global__ void __launch_bounds__(kBwdWarps * 32, kBwdBlocks)
     norm_rope_bwd_kernel(const RopeArgs a, const int blocks_q) {
+  extern __shared__ __align__(16) uint8_t smem[];
   const int b = blockIdx.x;
   const bool is_q = b < blocks_q;
+  // weight_grad_kernel may come up while this one runs; it waits for the partials
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const T *x = static_cast<const T *>(is_q ? a.q : a.k);
   const T *gy = static_cast<const T *>(is_q ? a.gq : a.gk);
   T *gx = static_cast<T *>(is_q ? a.q_out : a.k_out);
@@ -344,9 +380,9 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdBlocks)
   const int block = is_q ? b : b - blocks_q, blocks = is_q ? blocks_q : gridDim.x - blocks_q;
   if (w)
     bwd_kind<T, D, true>(a, x, gy, gx, x_rs, gy_rs, gx_rs, heads, w, block, blocks,
-                         a.gw_part + (int64_t)b * D);
+                         a.gw_part + (int64_t)b * D, smem);
   else
-    bwd_kind<T, D, false>(a, x, gy, gx, x_rs, gy_rs, gx_rs, heads, w, block, blocks, nullptr);
+    bwd_kind<T, D, false>(a, x, gy, gx, x_rs, gy_rs, gx_rs, heads, w, block, blocks, nullptr, smem);
 }
 
 // gw = sum of the blocks' partials, in a fixed order; 32 columns a block, the
@@ -357,6 +393,9 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const RopeArgs a, int
   const int col = threadIdx.x & 31, grp = threadIdx.x >> 5;
   const bool is_q = blockIdx.x < D / 32;
   T *dst = static_cast<T *>(is_q ? a.q_gw : a.k_gw);
+  // until the gradient kernel has finished; every block, so that this grid, and
+  // with it the call, does not end before that one
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!dst) return;
   const int i = blockIdx.x % (D / 32) * 32 + col;
   float v = 0.f;
@@ -398,19 +437,34 @@ template <typename T, int D>
 cudaError_t bwd(const RopeArgs &a, int sms, cudaStream_t st) {
   // blocks for queries and keys by their heads; no more than there are tokens for
   const int64_t want = ((int64_t)a.rows + kBwdWarps - 1) / kBwdWarps;
-  const int most = rope_bwd_blocks(sms), heads = a.hq + a.hkv;
+  // (a token's angles cost about as much as one group of heads)
+  constexpr int HPW = 32 / (D / 16);
+  const auto cost = [](int h) { return h == 0 ? 0 : (h + HPW - 1) / HPW + 1; };
+  const int most = rope_bwd_blocks(sms), all = cost(a.hq) + cost(a.hkv);
   const auto share = [&](int h) {
-    return h == 0 ? 0 : (int)std::min<int64_t>(want, std::max(1, (int)((int64_t)most * h / heads)));
+    return h == 0 ? 0 : (int)std::min<int64_t>(want, std::max<int64_t>(1, (int64_t)most * cost(h) / all));
   };
   const int blocks_q = share(a.hq), blocks = blocks_q + share(a.hkv);
   debug_log("norm+rotation backward: norm_rope_bwd_kernel d=%d, %d tokens, grid=%d (%d for queries)",
             D, a.rows, blocks, blocks_q);
+  cudaError_t e = set_smem_once<norm_rope_bwd_kernel<T, D>>(kBwdSmem);
+  if (e != cudaSuccess) return e;
   if (blocks > 0) {  // no tokens: the weights' gradients are empty sums
-    norm_rope_bwd_kernel<T, D><<<blocks, kBwdWarps * 32, 0, st>>>(a, blocks_q);
+    norm_rope_bwd_kernel<T, D><<<blocks, kBwdWarps * 32, kBwdSmem, st>>>(a, blocks_q);
     count_launches(1);
   }
   if (a.q_weight || a.k_weight) {
-    weight_grad_kernel<T, D><<<2 * D / 32, 1024, 0, st>>>(a, blocks_q, blocks);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * D / 32);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = blocks > 0;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, weight_grad_kernel<T, D>, a, blocks_q, blocks);
+    if (e != cudaSuccess) return e;
     count_launches(1);
   }
   return cudaGetLastError();

@@ -138,6 +138,21 @@ __device__ __forceinline__ void cp_async_8(void *dst, const void *src, uint32_t 
                : "memory");
 }
 
+// 16-byte global -> shared copy; src_bytes = 0 writes zeros and reads nothing.
+__device__ __forceinline__ void cp_async_16(void *dst, const void *src, uint32_t src_bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(src_bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All but the newest N committed groups of this thread have landed.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // The mbarrier's current phase also waits for this thread's cp.async copies
 // issued so far (the pending count is raised now and lowered when they land).
 __device__ __forceinline__ void cp_async_mbar_arrive(uint64_t *bar) {

@@ -104,15 +104,18 @@ def _check(status: int, what: str):
 
 
 _torch_module = None
+_raw_stream = None
 
 
 def _torch():
     """torch, imported at the first use (host-only calls do without it)."""
-    global _torch_module
+    global _torch_module, _raw_stream
     if _torch_module is None:
         import torch
 
         _torch_module = torch
+        # (the stream's handle without a Stream object around it: 3 us less a call)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     return _torch_module
 
 
@@ -132,10 +135,9 @@ def _p(t):
 def _stream():
     """Handle of the current device's current stream."""
     torch = _torch()
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None:
+    if _raw_stream is None:
         return torch.cuda.current_stream().cuda_stream
-    return raw(torch.cuda.current_device())  # without building a Stream object: 3 us less a call
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _need(cond, msg):
@@ -428,22 +430,9 @@ def fwd_fp8(q, k, v, descale_q=1.0, descale_k=1.0, descale_v=1.0, *, scale=None,
 # (The checks below are written out, with their messages made only when they
 # fail: on small calls the host's time is the call's time.)
 
-class _Same:
-    """No device change: the tensors' device is current already."""
-
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
-
-
-_SAME = _Same()
-
-
-def _on_device(*ts):
-    """The tensors lie on one CUDA device; a guard that makes it current (the
-    calls below then run on that device's current stream)."""
+def _call(name, args, ts):
+    """Makes the call `name` with `args` and, last, the current stream of the one
+    CUDA device that the tensors ts (None: absent) lie on."""
     index = None
     for t in ts:
         if t is not None:
@@ -455,7 +444,13 @@ def _on_device(*ts):
                     raise ValueError("tensors must be on one device")
                 index = i
     cuda = _torch().cuda
-    return _SAME if index == cuda.current_device() else cuda.device(index)
+    if index == cuda.current_device():
+        st = getattr(lib(), name)(*args, _stream())
+    else:
+        with cuda.device(index):
+            st = getattr(lib(), name)(*args, _stream())
+    if st != 0:
+        raise AttnError(st, name)
 
 
 def _contig(*ts):
@@ -516,10 +511,11 @@ def _cache_args(k_cache, v_cache, cu_seqlens, cache_seqlens, block_table):
 def paged_workspace(q, k_cache, batch, num_splits=0):
     """Scratch memory of fwd_paged for these queries and this cache."""
     rows, hq, d = q.shape
-    with _on_device(q):
+    torch = _torch()
+    _need(q.is_cuda, "tensors must be on a CUDA device")
+    with torch.cuda.device(q.device):
         n = lib().attn_fwd_paged_workspace_size(int(batch), rows, hq, k_cache.shape[2], d,
                                                 int(num_splits))
-    torch = _torch()
     return torch.empty(max(n, 1), device=q.device, dtype=torch.uint8)
 
 
@@ -549,16 +545,13 @@ def fwd_paged(q, k_cache, v_cache, cu_seqlens_q, cache_seqlens, *, block_table=N
         workspace = paged_workspace(q, k_cache, batch, num_splits)
     _contig(out, lse, workspace)
     wl, wr = window
-    with _on_device(q, k_cache, v_cache, cu_seqlens_q, cache_seqlens, block_table, out, lse,
-                    workspace):
-        st = lib().attn_fwd_paged(_p(q), _p(k_cache), _p(v_cache), _p(out), _p(lse),
-                                  _packed_stride(q), _page_stride(k_cache), _page_stride(v_cache),
-                                  _p(cu_seqlens_q), _p(cache_seqlens), _p(block_table), num_pages,
-                                  page_size, max_pages, 1 if appended else 0, batch, rows, _dt(q),
-                                  hq, hkv, d, _scale(scale, d), 1 if causal else 0, int(wl),
-                                  int(wr), softcap, num_splits, _p(workspace), workspace.nbytes,
-                                  _stream())
-    _check(st, "attn_fwd_paged")
+    _call("attn_fwd_paged",
+          (_p(q), _p(k_cache), _p(v_cache), _p(out), _p(lse), _packed_stride(q),
+           _page_stride(k_cache), _page_stride(v_cache), _p(cu_seqlens_q), _p(cache_seqlens),
+           _p(block_table), num_pages, page_size, max_pages, 1 if appended else 0, batch, rows,
+           _dt(q), hq, hkv, d, _scale(scale, d), 1 if causal else 0, int(wl), int(wr), softcap,
+           num_splits, _p(workspace), workspace.nbytes),
+          (q, k_cache, v_cache, cu_seqlens_q, cache_seqlens, block_table, out, lse, workspace))
     return out, lse
 
 
@@ -643,13 +636,11 @@ def qk_norm_rope(q, k, *, phases=None, positions=None, interleaved=False, q_weig
     ref, b, s, hq, hkv, d = _qk_sizes(q, k)
     rot = _rope_args(phases, q_weight, k_weight, ref)
     q_out, k_out = _result(q_out, q, "q_out"), _result(k_out, k, "k_out")
-    with _on_device(q, k, q_out, k_out, phases, positions, q_weight, k_weight):
-        st = lib().attn_qk_norm_rope(_p(q), _p(k), _p(q_out), _p(k_out), _row_stride(q),
-                                     _row_stride(k), _row_stride(q_out), _row_stride(k_out),
-                                     _p(q_weight), _p(k_weight), eps, _p(phases), rot,
-                                     1 if interleaved else 0, _positions(positions, b, s),
-                                     _dt(ref), b, s, hq, hkv, d, _stream())
-    _check(st, "attn_qk_norm_rope")
+    _call("attn_qk_norm_rope",
+          (_p(q), _p(k), _p(q_out), _p(k_out), _row_stride(q), _row_stride(k),
+           _row_stride(q_out), _row_stride(k_out), _p(q_weight), _p(k_weight), eps, _p(phases),
+           rot, 1 if interleaved else 0, _positions(positions, b, s), _dt(ref), b, s, hq, hkv, d),
+          (q, k, q_out, k_out, phases, positions, q_weight, k_weight))
     return q_out, k_out
 
 
@@ -657,7 +648,8 @@ def qk_norm_rope_bwd_workspace(q, k):
     """Scratch memory of qk_norm_rope_bwd for these queries and keys."""
     torch = _torch()
     ref, b, s, hq, hkv, d = _qk_sizes(q, k)
-    with _on_device(ref):
+    _need(ref.is_cuda, "tensors must be on a CUDA device")
+    with torch.cuda.device(ref.device):
         n = lib().attn_qk_norm_rope_bwd_workspace_size(b, s, hq, hkv, d)
     return torch.empty(max(n, 1), device=ref.device, dtype=torch.uint8)
 
@@ -682,16 +674,14 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, *, phases=None, positions=None, inter
     if workspace is None:
         workspace = qk_norm_rope_bwd_workspace(q, k)
     _contig(dq_out, dk_out, dq_weight, dk_weight, workspace)
-    with _on_device(q, k, dq_out, dk_out, dq, dk, phases, positions, q_weight, k_weight, dq_weight,
-                    dk_weight, workspace):
-        st = lib().attn_qk_norm_rope_bwd(_p(q), _p(k), _p(dq_out), _p(dk_out), _p(dq), _p(dk),
-                                         _row_stride(q), _row_stride(k), _row_stride(dq),
-                                         _row_stride(dk), _p(q_weight), _p(k_weight),
-                                         _p(dq_weight), _p(dk_weight), eps, _p(phases), rot,
-                                         1 if interleaved else 0, _positions(positions, b, s),
-                                         _dt(ref), b, s, hq, hkv, d, _p(workspace),
-                                         workspace.nbytes, _stream())
-    _check(st, "attn_qk_norm_rope_bwd")
+    _call("attn_qk_norm_rope_bwd",
+          (_p(q), _p(k), _p(dq_out), _p(dk_out), _p(dq), _p(dk), _row_stride(q), _row_stride(k),
+           _row_stride(dq), _row_stride(dk), _p(q_weight), _p(k_weight), _p(dq_weight),
+           _p(dk_weight), eps, _p(phases), rot, 1 if interleaved else 0,
+           _positions(positions, b, s), _dt(ref), b, s, hq, hkv, d, _p(workspace),
+           workspace.nbytes),
+          (q, k, dq_out, dk_out, dq, dk, phases, positions, q_weight, k_weight, dq_weight,
+           dk_weight, workspace))
     return dq, dk, dq_weight, dk_weight
 
 
@@ -717,15 +707,12 @@ def kvcache_append(k_new, v_new, k_cache, v_cache, cu_seqlens, cache_seqlens, *,
         q_out = _result(q_out, q, "q_out")
         _contig(q_out)
     rot = _rope_args(phases, q_weight, k_weight, k_new)
-    with _on_device(k_new, v_new, k_cache, v_cache, cu_seqlens, cache_seqlens, block_table, q,
-                    q_out, phases, q_weight, k_weight):
-        st = lib().attn_kvcache_append(_p(q), _p(q_out), _p(k_new), _p(v_new), _packed_stride(q),
-                                       _packed_stride(k_new), _packed_stride(v_new), _p(k_cache),
-                                       _p(v_cache), _page_stride(k_cache), _page_stride(v_cache),
-                                       _p(cu_seqlens), _p(cache_seqlens), _p(block_table),
-                                       num_pages, page_size, max_pages, _p(q_weight),
-                                       _p(k_weight), eps, _p(phases), rot,
-                                       1 if interleaved else 0, _dt(k_new), batch, total, hq, hkv,
-                                       d, _stream())
-    _check(st, "attn_kvcache_append")
+    _call("attn_kvcache_append",
+          (_p(q), _p(q_out), _p(k_new), _p(v_new), _packed_stride(q), _packed_stride(k_new),
+           _packed_stride(v_new), _p(k_cache), _p(v_cache), _page_stride(k_cache),
+           _page_stride(v_cache), _p(cu_seqlens), _p(cache_seqlens), _p(block_table), num_pages,
+           page_size, max_pages, _p(q_weight), _p(k_weight), eps, _p(phases), rot,
+           1 if interleaved else 0, _dt(k_new), batch, total, hq, hkv, d),
+          (k_new, v_new, k_cache, v_cache, cu_seqlens, cache_seqlens, block_table, q, q_out, phases,
+           q_weight, k_weight))
     return q_out
