@@ -157,8 +157,8 @@ __device__ __forceinline__ Token find_token(const RopeArgs &a, int r) {
   }
   tk.live = true;
   tk.pos = (int64_t)cached + (r - first);
-  const int64_t pg = tk.pos / a.page_size;
-  if (pg >= a.max_pages) {
+  const uint32_t pg = (uint32_t)tk.pos / (uint32_t)a.page_size;  // pos < 2^31 + 2^25
+  if (pg >= (uint32_t)a.max_pages) {
     if (lane == 0) raise_error(a.err, kErrCacheOverflow);
     return tk;
   }
@@ -169,7 +169,7 @@ __device__ __forceinline__ Token find_token(const RopeArgs &a, int r) {
   }
   tk.cached = true;
   tk.page = page;
-  tk.slot = (int)(tk.pos - pg * a.page_size);
+  tk.slot = (int)((uint32_t)tk.pos - pg * a.page_size);
   return tk;
 }
 
@@ -179,31 +179,15 @@ template <typename T, int D, bool kAppend>
 __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const RopeArgs a) {
   constexpr int LPH = D / 16, HPW = 32 / LPH;
   const int lane = threadIdx.x & 31, t = lane % LPH, sub = lane / LPH;
-  const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t row = unit / a.parts;
-  if (row >= a.rows) return;
-  const int part = (int)(unit % a.parts);
-  int64_t pos;
-  T *kd = nullptr, *vd = nullptr;
-  if constexpr (kAppend) {
-    const Token tk = find_token(a, (int)row);
-    if (!tk.live) return;
-    pos = tk.pos;
-    if (tk.cached) {
-      const int64_t in_page = (int64_t)tk.slot * a.hkv * D;
-      kd = static_cast<T *>(a.k_out) + tk.page * a.k_out_rs + in_page;
-      vd = static_cast<T *>(a.v_out) + tk.page * a.v_out_rs + in_page;
-    }
-  } else {
-    pos = a.positions ? a.positions[row] : row % a.s;
-    kd = static_cast<T *>(a.k_out) + row * a.k_out_rs;
-  }
+  // (rows * parts fits 32 bits: more than one part only where there are few rows)
+  const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const uint32_t row = unit / (uint32_t)a.parts;
+  if (row >= (uint32_t)a.rows) return;
+  const int part = (int)(unit - row * a.parts);
   T *qd = static_cast<T *>(a.q_out) + row * a.q_out_rs;
   const T *qs = static_cast<const T *>(a.q) + row * a.q_rs;
   const T *ks = static_cast<const T *>(a.k) + row * a.k_rs;
   const Slots sl = slots_of(t, a.rot, a.interleaved);
-  float c[8], s[8];
-  if (sl.turn) angles(a.phases, t, pos, c, s);
   const int nq = (a.hq + HPW - 1) / HPW, nk = (a.hkv + HPW - 1) / HPW;
   const int n = nq + nk * (kAppend ? 2 : 1);
   // group it: heads HPW it' .. of the queries, keys or values (kind 0, 1, 2)
@@ -218,7 +202,24 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const RopeArgs a
     return load_raw(src + h * D, k == 2 ? Slots{16 * t, 16 * t + 8, false} : sl,
                     h < (k == 0 ? a.hq : a.hkv));
   };
-  Raw next = load(part);
+  Raw next = load(part);  // on its way while the token's place is looked up
+  int64_t pos;
+  T *kd = nullptr, *vd = nullptr;
+  if constexpr (kAppend) {
+    const Token tk = find_token(a, (int)row);
+    if (!tk.live) return;
+    pos = tk.pos;
+    if (tk.cached) {
+      const int64_t in_page = (int64_t)tk.slot * a.hkv * D;
+      kd = static_cast<T *>(a.k_out) + tk.page * a.k_out_rs + in_page;
+      vd = static_cast<T *>(a.v_out) + tk.page * a.v_out_rs + in_page;
+    }
+  } else {
+    pos = a.positions ? (int64_t)a.positions[row] : (int64_t)(row % (uint32_t)a.s);
+    kd = static_cast<T *>(a.k_out) + row * a.k_out_rs;
+  }
+  float c[8], s[8];
+  if (sl.turn) angles(a.phases, t, pos, c, s);
   for (int it = part; it < n; it += a.parts) {
     const Raw now = next;
     next = load(it + a.parts);
