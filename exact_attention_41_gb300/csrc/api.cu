@@ -583,7 +583,8 @@ attn_status attn_fwd_paged(const void *q, const void *k_cache, const void *v_cac
   a.stall = test_stall();
   a.pack = plan.pack;
   a.num_splits = plan.num_splits;
-  a.target = plan.target;
+  a.wave = plan.wave;
+  a.max_waves = plan.max_waves;
   a.slots = (int)plan.slots;
   a.o_part = static_cast<float *>(workspace);
   a.lse_part = a.o_part + plan.slots * 128 * plan.layout * d;

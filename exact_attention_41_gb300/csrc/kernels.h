@@ -88,12 +88,12 @@ struct PagedArgs {
   int *err;
   uint64_t wait_ns;             // wall-clock limit of a device-side wait (ns)
   int stall;                    // test hook, as FwdArgs::stall
-  // work split (paged_plan): num_splits 0 cuts the keys into about `target`
-  // pieces of equal length over the whole call, 1 does not cut, n > 1 cuts
-  // every row's keys into n pieces.  Pieces of cut rows write their partial
-  // results to one of `slots` slots of the workspace.
+  // work split (paged_plan): num_splits 0 cuts the keys into pieces of about
+  // equal length over the whole call, by the `wave` of blocks that the GPU holds
+  // at a time; 1 does not cut, n > 1 cuts every row's keys into n pieces.  Pieces
+  // of cut rows write partial results to one of `slots` slots of the workspace.
   int pack;                     // query heads that share a tile: g or 1
-  int num_splits, target, slots;
+  int num_splits, wave, max_waves, slots;
   float *o_part;                // (slots, rows of a block, d)
   float *lse_part;              // (slots, rows of a block), log2 units
 };
@@ -103,7 +103,7 @@ struct PagedPlan {
   int layout;                   // query tiles of 128 rows per block
   int pack;
   int tile_pos;                 // query positions of one 128-row tile
-  int num_splits, target;
+  int num_splits, wave, max_waves;
   int64_t tiles, items, slots;  // tiles x heads; with pieces: blocks of the grid; partial results
   size_t ws_bytes;
 };

@@ -47,6 +47,7 @@ constexpr int kBM = 128;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O when max grows > 256x
 constexpr int kMaxStages = 5;
 constexpr int kMinPieceSteps = 4;          // shortest piece worth a block and a partial result
+constexpr int kBlockSteps = 8;             // a block's start and end, in steps
 
 // NT query tiles per block, BN keys per step, as FwdCfg in the dense forward.
 template <int D, int BN, int NT>
@@ -133,14 +134,48 @@ __device__ __forceinline__ bool find_item(const PagedArgs &a, uint32_t idx, int 
   if (a.num_splits == 0) {
     // (fp32: the sums need no more than the order of magnitude, and both
     // kernels add in the same order)
-    float work = (float)first.tiles * (float)first.steps;
+    float work = (float)first.tiles * (float)first.steps, pairs = (float)first.tiles;
     for (int b0 = 32; b0 < a.batch; b0 += 32) {
       const Shape x = shape(b0 + lane);
       work += (float)x.tiles * (float)x.steps;
+      pairs += (float)x.tiles;
     }
     work = warp_sum(work) * (float)nh;
-    // at least work / target even after rounding, so that cut pieces fit the slots
-    piece_steps = max(kMinPieceSteps, (int)fminf(work / (float)a.target * 1.0001f, 1e9f) + 1);
+    pairs = warp_sum(pairs) * (float)nh;
+    // least piece that makes about n full ones
+    const auto least = [&](float n) {
+      return max(kMinPieceSteps, (int)fminf(work / n * 1.0001f, 1e9f) + 1);
+    };
+    // Pieces make waves of blocks, and a wave that is started for a few of them
+    // is lost.  Pairs end in a part of a piece, half of one on average: n full
+    // pieces make n + pairs / 2.  Take the number of waves whose time -- a
+    // piece's steps, and kBlockSteps for a block's start and end -- is least.
+    // (24 sequences of 2-9 tokens, d = 64: 2.3 waves 127 us, just below two 109.)
+    piece_steps = least(2.f * (float)a.wave);  // more pairs than kmax waves
+    float best = INFINITY, room = 0.f;
+    for (int k = 1; k <= a.max_waves; ++k) {
+      const float blocks = (float)k * (float)a.wave;
+      if (pairs >= 0.9f * blocks) continue;
+      const int ps = least(0.98f * blocks - 0.5f * pairs);
+      const float time = (float)k * (float)(ps + kBlockSteps);
+      if (time < best) {
+        best = time;
+        piece_steps = ps;
+        room = blocks;
+      }
+    }
+    if (room > 0.f) {
+      // The average may be off, and the grid has to hold every item.  It holds
+      // all pairs and two waves of full pieces where max_waves is 3; else, and
+      // where the pieces of up to 32 sequences show that they miss the wave, the
+      // size that fits in any case.
+      if (a.batch > 32 && a.max_waves == 3) {
+        piece_steps = max(piece_steps, least(2.f * (float)a.wave));
+      } else {
+        const float n = (float)first.tiles * (float)((first.steps + piece_steps - 1) / piece_steps);
+        if (a.batch > 32 || warp_sum(n) * (float)nh > room) piece_steps = least(room - pairs);
+      }
+    }
   }
   uint32_t base = 0, slots = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
@@ -216,6 +251,25 @@ __device__ __forceinline__ Piece piece_of(const PagedArgs &a, const Item &it, in
   return p;
 }
 
+// Pages and slots of the piece's key boxes b0 .. b0 + 31, one per lane.  The
+// producers keep 32 in hand and the next 32 on their way: a look-up per step
+// would add a trip to L2 or further to it.
+struct Box {
+  int page, slot;  // page -1: no visible key, -2: outside the pool
+};
+__device__ __forceinline__ Box fetch_boxes(const PagedArgs &a, const Item &it, const Piece &p,
+                                           int boxes, int box_rows, int key_lo, int b0) {
+  Box x{-1, 0};
+  const int b = b0 + (threadIdx.x & 31), row0 = key_lo + b * box_rows;
+  if (b < p.nt * boxes && row0 < p.ke && row0 + box_rows > p.kb) {
+    const int lp = a.block_table ? row0 / a.page_size : 0;
+    x.slot = row0 - lp * a.page_size;
+    x.page = paged_page(a, it.seq, lp);
+    if (x.page < 0) x.page = -2;
+  }
+  return x;
+}
+
 struct Shared {
   uint64_t q_full;
   uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
@@ -264,11 +318,13 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
   const int pg = a.pack;
   // the combine kernel may start to find its tiles as soon as there is room
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  Box early{-1, 0};  // the K producer's first boxes, on their way before the others start
   if (warp == 0) {
     Item it{};
     it.pieces = 1;
     const bool found = find_item(a, blockIdx.x, tile_pos * NT, BN, false, blockIdx.x == 0, it);
     const Piece p = piece_of(a, it, tile_pos * NT, BN, found);
+    early = fetch_boxes(a, it, p, BN / box_rows, box_rows, p.n_lo * BN, 0);
     if (lane == 0) {
       sh.item = it;
       sh.piece = p;
@@ -340,23 +396,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
         const int box = lane / C::kCols, col = lane % C::kCols;  // this lane's part of a tile
         const int key_lo = n_lo * BN;
         uint8_t *dst = (is_v ? v_s : k_s) + col * (BN * 128) + box * box_rows * 128;
-        // Pages and slots of 32 boxes at a time, one per lane, and of the next
-        // 32 ahead: a look-up per step would add a trip to L2 or further to it.
-        struct Box {
-          int page, slot;  // page -1: no visible key, -2: outside the pool
-        };
-        auto fetch = [&](int b0) {
-          Box x{-1, 0};
-          const int row0 = key_lo + (b0 + lane) * box_rows;
-          if (b0 + lane < nt * boxes && row0 < pc.ke && row0 + box_rows > pc.kb) {
-            const int lp = a.block_table ? row0 / a.page_size : 0;
-            x.slot = row0 - lp * a.page_size;
-            x.page = paged_page(a, it.seq, lp);
-            if (x.page < 0) x.page = -2;
-          }
-          return x;
-        };
-        Box now{-1, 0}, ahead = fetch(0);
+        Box now{-1, 0}, ahead = is_v ? fetch_boxes(a, it, pc, boxes, box_rows, key_lo, 0) : early;
         if (!is_v && lane == 0) {
           mbar_expect_tx(&sh.q_full, NT * tile_pos * pg * D * 2);
           for (int t = 0; t < NT; ++t)
@@ -391,7 +431,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
               }
               break;
             }
-            ahead = fetch(j * boxes + 32);
+            ahead = fetch_boxes(a, it, pc, boxes, box_rows, key_lo, j * boxes + 32);
           }
           const int page = __shfl_sync(0xffffffffu, now.page, (in32 + box) & 31);
           const int slot = __shfl_sync(0xffffffffu, now.slot, (in32 + box) & 31);
@@ -703,30 +743,31 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
       T *orow = static_cast<T *>(a.o) + ((int64_t)(sq.q0 + i) * a.hq + hr) * D;
       const int64_t part = (int64_t)it.slot * (NT * kBM) + t * kBM + r;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t u[32];
+      for (int c2 = 0; c2 < D / 64; ++c2) {
+        uint32_t u[64];
         if (ok && ntt > 0) {
-          tmem_ld32(o_t + c * 32, u);
+          tmem_ld32(o_t + c2 * 64, *reinterpret_cast<uint32_t(*)[32]>(u));
+          tmem_ld32(o_t + c2 * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(u + 32));
           tmem_wait_ld();
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) u[e] = 0u;
+          for (int e = 0; e < 64; ++e) u[e] = 0u;
         }
         if (it.pieces == 1) {
-          uint32_t w[16];
+          uint32_t w[32];
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
+          for (int e = 0; e < 32; ++e)
             w[e] = Elem<T>::from_f2(__uint_as_float(u[2 * e]) * inv, __uint_as_float(u[2 * e + 1]) * inv);
           if (valid) {
-            uint4 *dst = reinterpret_cast<uint4 *>(orow + c * 32);
+            uint4 *dst = reinterpret_cast<uint4 *>(orow + c2 * 64);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < 8; ++e)
               dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
           }
         } else if (valid && it.slot < a.slots) {
-          float4 *dst = reinterpret_cast<float4 *>(a.o_part + part * D + c * 32);
+          float4 *dst = reinterpret_cast<float4 *>(a.o_part + part * D + c2 * 64);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
+          for (int e = 0; e < 16; ++e)
             dst[e] = make_float4(__uint_as_float(u[4 * e]) * inv, __uint_as_float(u[4 * e + 1]) * inv,
                                  __uint_as_float(u[4 * e + 2]) * inv,
                                  __uint_as_float(u[4 * e + 3]) * inv);
@@ -849,8 +890,8 @@ cudaError_t paged(const PagedArgs &a, const PagedPlan &plan, cudaStream_t st) {
     e = check_regs_once<paged_tc_kernel<T, D, BN, NT>>(C::kThreads, 128 * 88 + 256 * 208);
   if (e != cudaSuccess) return e;
   debug_log("paged: paged_tc_kernel d=%d, %d query tile(s) of 128 rows per block, %d-key tiles in "
-            "boxes of %d, pack=%d, num_splits=%d (target %d), grid=%lld x %d threads, smem=%d B",
-            D, NT, BN, box_rows, a.pack, a.num_splits, a.target, (long long)plan.items, C::kThreads,
+            "boxes of %d, pack=%d, num_splits=%d (wave %d), grid=%lld x %d threads, smem=%d B",
+            D, NT, BN, box_rows, a.pack, a.num_splits, a.wave, (long long)plan.items, C::kThreads,
             C::kSmem);
   paged_tc_kernel<T, D, BN, NT><<<(unsigned)plan.items, C::kThreads, C::kSmem, st>>>(
       tq, tk, tv, a, plan.tile_pos, box_rows);
@@ -896,12 +937,17 @@ PagedPlan paged_plan(int batch, int total_q, int hq, int hkv, int d, int num_spl
   p.num_splits = num_splits;
   // enough tiles for several waves even if no sequence leaves one half empty
   if (num_splits == 0 && (int64_t)(total_q + pos - 1) / pos * nh >= 4 * wave) p.num_splits = 1;
-  p.target = (int)(2 * wave);
+  p.wave = (int)wave;
   if (p.num_splits == 0) {
-    // cut pieces: below 2 target (each cut tile has at least one piece of full
-    // length, and full pieces are at most target)
-    p.items = p.tiles + p.target;
-    p.slots = std::min<int64_t>(2 * (int64_t)p.target, p.items);
+    // few pairs divide evenly into one wave; many leave ragged pieces, which
+    // even out over several (find_item).  Blocks behind the last item cost a
+    // start each, so no more than can be needed.
+    p.max_waves = p.tiles <= wave / 4 ? 1 : p.tiles <= wave / 2 ? 2 : 3;
+    p.items = p.max_waves * wave;
+    // more pairs than that: pieces of work / (2 waves), at most 2 waves of full
+    // ones and one more per pair; of cut pairs at most twice as many as full ones
+    if (p.max_waves == 3) p.items = std::max(p.items, p.tiles + 2 * wave);
+    p.slots = std::min(4 * wave, p.items);
   } else {
     p.items = p.tiles * p.num_splits;
     p.slots = p.num_splits > 1 ? p.items : 0;
