@@ -519,7 +519,7 @@ size_t attn_fwd_paged_workspace_size(int batch, int total_q, int hq, int hkv, in
   if (batch <= 0 || total_q <= 0 || hkv <= 0 || hq < hkv || hq % hkv || d <= 0 || num_splits < 0)
     return 0;
   const DeviceInfo *di = device_info();
-  return paged_plan(batch, total_q, hq, hkv, d, num_splits, di ? di->sms : 152).ws_bytes;
+  return paged_plan(batch, total_q, hq, hkv, d, num_splits, INT32_MAX, di ? di->sms : 152).ws_bytes;
 }
 
 attn_status attn_fwd_paged(const void *q, const void *k_cache, const void *v_cache, void *out,
@@ -546,7 +546,8 @@ attn_status attn_fwd_paged(const void *q, const void *k_cache, const void *v_cac
   if ((int64_t)total_q * hq > INT32_MAX || hq > 65535) return ATTN_ERR_UNSUPPORTED;
   const DeviceInfo *di = device_info();
   const PagedPlan plan =
-      paged_plan(batch, total_q, hq, hkv, d, num_splits, di ? di->sms : 152);
+      paged_plan(batch, total_q, hq, hkv, d, num_splits, (int64_t)max_pages_per_seq * page_size,
+                 di ? di->sms : 152);
   if (plan.items > INT32_MAX || plan.slots > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
   if (plan.ws_bytes > 0 && (!workspace || workspace_bytes < plan.ws_bytes))
     return ATTN_ERR_WORKSPACE;
@@ -588,6 +589,7 @@ attn_status attn_fwd_paged(const void *q, const void *k_cache, const void *v_cac
   a.slots = (int)plan.slots;
   a.o_part = static_cast<float *>(workspace);
   a.lse_part = a.o_part + plan.slots * 128 * plan.layout * d;
+  a.written = reinterpret_cast<int *>(a.lse_part + plan.slots * 128 * plan.layout);
   if (num_pages == 0 || (block_table && page_size % 16 != 0))
     return launched(launch_paged_simt(a, stream));
   return launched(launch_paged_tc(a, plan, stream));

@@ -96,6 +96,7 @@ struct PagedArgs {
   int num_splits, wave, max_waves, slots;
   float *o_part;                // (slots, rows of a block, d)
   float *lse_part;              // (slots, rows of a block), log2 units
+  int *written;                 // (slots) pieces written, at a pair's first slot
 };
 
 // How attn_fwd_paged cuts its work; host only, from the sizes of the call.
@@ -107,7 +108,9 @@ struct PagedPlan {
   int64_t tiles, items, slots;  // tiles x heads; with pieces: blocks of the grid; partial results
   size_t ws_bytes;
 };
-PagedPlan paged_plan(int batch, int total_q, int hq, int hkv, int d, int num_splits, int sms);
+// keys: most keys of a sequence
+PagedPlan paged_plan(int batch, int total_q, int hq, int hkv, int d, int num_splits, int64_t keys,
+                     int sms);
 
 // Per-head norm and rotation (attn_qk_norm_rope, its backward, and
 // attn_kvcache_append).  *_rs: elements between consecutive token rows; for

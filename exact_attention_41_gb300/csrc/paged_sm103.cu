@@ -19,7 +19,8 @@
 // Pieces.  With few query rows the keys are cut so that the call fills the
 // GPU: all sequences' key steps together, divided by the wanted number of
 // items, give the length of a piece.  Pieces of a cut row write a normalised
-// fp32 O and its log2-sum; paged_combine_kernel joins them in piece order.
+// fp32 O and its log2-sum; the block that writes the last piece of a tile joins
+// them, in piece order.
 //
 // Keys.  A K or V tile of BN keys is one TMA box where a page holds a multiple
 // of BN keys, and otherwise one box per gcd(page_size, BN) keys, issued by as
@@ -46,8 +47,10 @@ using namespace sm103;
 constexpr int kBM = 128;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O when max grows > 256x
 constexpr int kMaxStages = 5;
+constexpr int kMaxWarps = 12;
 constexpr int kMinPieceSteps = 4;          // shortest piece worth a block and a partial result
 constexpr int kBlockSteps = 8;             // a block's start and end, in steps
+constexpr int kJoinSteps = 4;              // what joining pieces adds to a call, in steps
 
 // NT query tiles per block, BN keys per step, as FwdCfg in the dense forward.
 template <int D, int BN, int NT>
@@ -105,77 +108,105 @@ __device__ __forceinline__ uint32_t add_sat(uint32_t x, uint32_t y) {
   return min(x + y, (uint32_t)INT32_MAX);  // both at most INT32_MAX
 }
 
+// A sequence's tiles and longest key range, in steps.
+struct Shape {
+  int tiles, steps;
+};
+__device__ __forceinline__ Shape shape_of(const PagedArgs &a, const PagedSeq &s, int pos, int bn) {
+  Shape x{(s.lq + pos - 1) / pos, 0};
+  if (x.tiles > 0) x.steps = key_steps(a, s, (x.tiles - 1) * pos, pos, bn).nt;
+  if (x.tiles > 1) x.steps = max(x.steps, key_steps(a, s, 0, pos, bn).nt);
+  return x;
+}
+
+// The shapes of all sequences, in shared memory for the first kMaxShapes (the
+// tiles' own space, which no copy uses yet), and sums over all of them.
+constexpr int kMaxShapes = 4096;
+constexpr int kMaxSplits = 1024;  // their weights have to fit shared memory
+struct Shapes {
+  Shape *at;
+  float work, pairs;  // per head: key steps; tiles
+  int longest;        // steps
+};
+// One warp's share, sequences `warp` * 32 + lane and on by `warps` * 32; returns
+// its part of the sums.  raise: report bad lengths.
+__device__ __forceinline__ Shapes gather_shapes(const PagedArgs &a, Shape *at, int warp, int warps,
+                                                int pos, int bn, bool raise) {
+  float work = 0.f, pairs = 0.f;
+  int longest = 0;
+  for (int i = warp * 32 + (threadIdx.x & 31); i < a.batch; i += warps * 32) {
+    const PagedSeq s = paged_seq(a, i);
+    if (raise && s.err) raise_error(a.err, s.err);
+    const Shape x = shape_of(a, s, pos, bn);
+    if (i < kMaxShapes) at[i] = x;
+    work += (float)x.tiles * (float)x.steps;
+    pairs += (float)x.tiles;
+    longest = max(longest, x.steps);
+  }
+  return Shapes{at, warp_sum(work), warp_sum(pairs), __reduce_max_sync(0xffffffffu, longest)};
+}
+
+// Key steps of a piece, where num_splits leaves the choice (all blocks compute
+// it alike).  pieces(ps): how many items pieces of ps steps make; asked once.
+template <typename F>
+__device__ __forceinline__ int choose_piece(const PagedArgs &a, float work, float pairs,
+                                            int longest, const F &pieces) {
+  // least piece that makes about n full ones
+  const auto least = [&](float n) {
+    return max(kMinPieceSteps, (int)fminf(work / n * 1.0001f, 1e9f) + 1);
+  };
+  // Pieces make waves of blocks, and a wave that is started for a few of them
+  // is lost.  Pairs of a tile and a head end in a part of a piece, half of one on
+  // average: n full pieces make n + pairs / 2.  Take the number of waves whose
+  // time -- a piece's steps, and kBlockSteps for a block's start and end -- is
+  // least.  (24 sequences of 2-9 tokens, d = 64: 2.3 waves 127 us, just below two
+  // 109.)
+  int ps = least(2.f * (float)a.wave);  // more pairs than max_waves hold
+  float best = INFINITY, room = 0.f;
+  for (int k = 1; k <= a.max_waves; ++k) {
+    const float blocks = (float)k * (float)a.wave;
+    if (pairs >= 0.9f * blocks) continue;
+    const int p = least(0.98f * blocks - 0.5f * pairs);
+    const float time = (float)k * (float)(p + kBlockSteps);
+    if (time < best) {
+      best = time;
+      ps = p;
+      room = blocks;
+    }
+  }
+  // Whole pairs, unless pieces and the joining of them are worth it.
+  if (ceilf(pairs / (float)a.wave) * (float)(longest + kBlockSteps) <= best + kJoinSteps)
+    return INT32_MAX;
+  // The average may be off, and the grid has to hold every item.  Where
+  // max_waves is 3 it holds all pairs and two waves of full pieces besides; else
+  // the size that fits in any case replaces one that misses the wave.
+  if (room > 0.f && pieces(ps) > room)
+    ps = a.max_waves == 3 && pairs >= 0.7f * room ? max(ps, least(2.f * (float)a.wave))
+                                                  : least(room - pairs);
+  return ps;
+}
+
 // Item `idx` of the call; false behind the last one.  Whole warp; `pos` query
-// positions per block.  whole: idx counts tiles, not their pieces, and the first
-// piece is found.  raise: report bad lengths (one block of the grid does).
-// Counts saturate at INT32_MAX, above every block index, so offsets that
-// overlap (more rows than total_q) only lose work, which is flagged.
-__device__ __forceinline__ bool find_item(const PagedArgs &a, uint32_t idx, int pos, int bn,
-                                          bool whole, bool raise, Item &it) {
+// positions per block.  Counts saturate at INT32_MAX, above every block index, so
+// offsets that overlap (more rows than total_q) only lose work, which is flagged.
+__device__ __forceinline__ bool find_item(const PagedArgs &a, const Shapes &sh, uint32_t idx,
+                                          int pos, int bn, Item &it) {
   const int lane = threadIdx.x & 31;
   const int nh = a.pack > 1 ? a.hkv : a.hq;
-  // tiles and longest key range of sequence i
-  struct Shape {
-    PagedSeq s;
-    int tiles, steps;
+  const auto shape = [&](int i) {
+    if (i >= a.batch) return Shape{0, 0};
+    return i < kMaxShapes ? sh.at[i] : shape_of(a, paged_seq(a, i), pos, bn);
   };
-  auto shape = [&](int i) {
-    Shape x{{0, 0, 0, 0}, 0, 0};
-    if (i < a.batch) {
-      x.s = paged_seq(a, i);
-      x.tiles = (x.s.lq + pos - 1) / pos;
-      if (x.tiles > 0) x.steps = key_steps(a, x.s, (x.tiles - 1) * pos, pos, bn).nt;
-      if (x.tiles > 1) x.steps = max(x.steps, key_steps(a, x.s, 0, pos, bn).nt);
-    }
-    return x;
-  };
-  const Shape first = shape(lane);
   int piece_steps = INT32_MAX;
   if (a.num_splits == 0) {
-    // (fp32: the sums need no more than the order of magnitude, and both
-    // kernels add in the same order)
-    float work = (float)first.tiles * (float)first.steps, pairs = (float)first.tiles;
-    for (int b0 = 32; b0 < a.batch; b0 += 32) {
-      const Shape x = shape(b0 + lane);
-      work += (float)x.tiles * (float)x.steps;
-      pairs += (float)x.tiles;
-    }
-    work = warp_sum(work) * (float)nh;
-    pairs = warp_sum(pairs) * (float)nh;
-    // least piece that makes about n full ones
-    const auto least = [&](float n) {
-      return max(kMinPieceSteps, (int)fminf(work / n * 1.0001f, 1e9f) + 1);
-    };
-    // Pieces make waves of blocks, and a wave that is started for a few of them
-    // is lost.  Pairs end in a part of a piece, half of one on average: n full
-    // pieces make n + pairs / 2.  Take the number of waves whose time -- a
-    // piece's steps, and kBlockSteps for a block's start and end -- is least.
-    // (24 sequences of 2-9 tokens, d = 64: 2.3 waves 127 us, just below two 109.)
-    piece_steps = least(2.f * (float)a.wave);  // more pairs than kmax waves
-    float best = INFINITY, room = 0.f;
-    for (int k = 1; k <= a.max_waves; ++k) {
-      const float blocks = (float)k * (float)a.wave;
-      if (pairs >= 0.9f * blocks) continue;
-      const int ps = least(0.98f * blocks - 0.5f * pairs);
-      const float time = (float)k * (float)(ps + kBlockSteps);
-      if (time < best) {
-        best = time;
-        piece_steps = ps;
-        room = blocks;
+    piece_steps = choose_piece(a, sh.work * (float)nh, sh.pairs * (float)nh, sh.longest, [&](int ps) {
+      float n = 0.f;
+      for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        const Shape x = shape(b0 + lane);
+        n += (float)x.tiles * (float)((x.steps + ps - 1) / ps);
       }
-    }
-    if (room > 0.f) {
-      // The average may be off, and the grid has to hold every item.  It holds
-      // all pairs and two waves of full pieces where max_waves is 3; else, and
-      // where the pieces of up to 32 sequences show that they miss the wave, the
-      // size that fits in any case.
-      if (a.batch > 32 && a.max_waves == 3) {
-        piece_steps = max(piece_steps, least(2.f * (float)a.wave));
-      } else {
-        const float n = (float)first.tiles * (float)((first.steps + piece_steps - 1) / piece_steps);
-        if (a.batch > 32 || warp_sum(n) * (float)nh > room) piece_steps = least(room - pairs);
-      }
-    }
+      return warp_sum(n) * (float)nh;
+    });
   }
   const auto pieces_of = [&](const Shape &x) {
     if (a.num_splits > 0) return max(1, min(a.num_splits, x.steps));
@@ -187,16 +218,13 @@ __device__ __forceinline__ bool find_item(const PagedArgs &a, uint32_t idx, int 
   // Order: sequences of several tiles are bound by the tensor cores, those of
   // one tile mostly by memory.  Where a call has both, their items alternate in
   // proportion, so that the two kinds of blocks run beside one another.
-  // (47 single tokens and a chunk of 2001: 285 us in sequence order.)
+  // (47 single tokens and a chunk of 2001: 285 us in sequence order, 266 so.)
   uint32_t n_long = 0, n_all = 0;
-  if (!whole) {
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-      const Shape x = b0 == 0 ? first : shape(b0 + lane);
-      if (raise && x.s.err) raise_error(a.err, x.s.err);
-      const uint32_t n = min(times(x, pieces_of(x)), 1u << 24);
-      n_all = add_sat(n_all, __reduce_add_sync(0xffffffffu, n));
-      n_long = add_sat(n_long, __reduce_add_sync(0xffffffffu, x.tiles > 1 ? n : 0));
-    }
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    const Shape x = shape(b0 + lane);
+    const uint32_t n = min(times(x, pieces_of(x)), 1u << 24);
+    n_all = add_sat(n_all, __reduce_add_sync(0xffffffffu, n));
+    n_long = add_sat(n_long, __reduce_add_sync(0xffffffffu, x.tiles > 1 ? n : 0));
   }
   const bool mixed = n_long > 0 && n_long < n_all && n_all < (1u << 16);
   bool is_long = false;
@@ -208,9 +236,9 @@ __device__ __forceinline__ bool find_item(const PagedArgs &a, uint32_t idx, int 
   }
   uint32_t base = 0, slots = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    const Shape x = b0 == 0 ? first : shape(b0 + lane);
+    const Shape x = shape(b0 + lane);
     const int pieces = pieces_of(x);
-    const uint32_t n = mixed && is_long != (x.tiles > 1) ? 0 : times(x, whole ? 1 : pieces);
+    const uint32_t all = times(x, pieces), n = mixed && is_long != (x.tiles > 1) ? 0 : all;
     uint32_t incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -218,28 +246,24 @@ __device__ __forceinline__ bool find_item(const PagedArgs &a, uint32_t idx, int 
       if (lane >= o) incl = add_sat(incl, up);
     }
     const uint32_t hit = __ballot_sync(0xffffffffu, idx < add_sat(base, incl));
-    const uint32_t cut = pieces > 1 ? times(x, pieces) : 0;  // slots
+    const uint32_t cut = pieces > 1 ? all : 0;  // slots
     if (hit) {
       const int src = __ffs(hit) - 1;
       slots = add_sat(slots, __reduce_add_sync(0xffffffffu, lane < src ? cut : 0));
       const uint32_t local = idx - base - __shfl_sync(0xffffffffu, incl - n, src);
       it.seq = b0 + src;
+      it.s = paged_seq(a, it.seq);
       it.pieces = __shfl_sync(0xffffffffu, pieces, src);
       const int tiles = __shfl_sync(0xffffffffu, x.tiles, src);
-      it.s.q0 = __shfl_sync(0xffffffffu, x.s.q0, src);
-      it.s.lq = __shfl_sync(0xffffffffu, x.s.lq, src);
-      it.s.lk = __shfl_sync(0xffffffffu, x.s.lk, src);
-      it.s.err = 0;
       // heads fastest (they share a sequence's pages and, in L2, its K and V),
       // then pieces; the last positions, which see the most keys, first
       const uint32_t upper = local / (uint32_t)nh;
       it.head = (int)(local - upper * nh);
-      const uint32_t m = whole ? upper : upper / (uint32_t)it.pieces;
-      it.piece = whole ? 0 : (int)(upper - m * it.pieces);
+      const uint32_t m = upper / (uint32_t)it.pieces;
+      it.piece = (int)(upper - m * it.pieces);
       it.m0 = (tiles - 1 - (int)m) * pos;
       // pieces of one tile and head are nh slots apart
-      const uint32_t at = (m * it.pieces + it.piece) * nh + it.head;
-      it.slot = it.pieces > 1 ? (int)add_sat(slots, at) : -1;
+      it.slot = it.pieces > 1 ? (int)add_sat(slots, local) : -1;
       return it.m0 >= 0;
     }
     base = add_sat(base, __shfl_sync(0xffffffffu, incl, 31));
@@ -251,10 +275,10 @@ __device__ __forceinline__ bool find_item(const PagedArgs &a, uint32_t idx, int 
 // One piece of an item in key steps.
 struct Piece {
   int n_lo, nt;     // first step and how many
+  int written;      // pieces of the pair that have a step (one if none has)
   int kb, ke;       // visible keys of the block's rows (of all pieces)
   int front, back;  // V rows of the first / last step outside [kb, ke)
-  int live;         // 0: behind the last item, or behind the last key (the
-                    // combine step skips such a piece by the same test)
+  int live;         // 0: behind the last item, or behind the last key
 };
 __device__ __forceinline__ Piece piece_of(const PagedArgs &a, const Item &it, int pos, int bn,
                                           bool found) {
@@ -263,6 +287,7 @@ __device__ __forceinline__ Piece piece_of(const PagedArgs &a, const Item &it, in
   const int lo = min(it.piece * per, all.nt);
   Piece p;
   p.live = found && (it.piece == 0 || lo < all.nt);
+  p.written = all.nt == 0 ? 1 : (all.nt + per - 1) / per;
   p.n_lo = all.n_lo + lo;
   p.nt = p.live ? min(all.nt - lo, per) : 0;
   p.kb = all.kb;
@@ -300,8 +325,10 @@ struct Shared {
   uint64_t wait_ns;
   Item item;
   Piece piece;
+  Shapes sums[kMaxWarps];  // of the warps' sequences
   uint32_t tmem_base;
   int abort;
+  int joins;               // this block joins the pair's pieces
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -320,6 +347,83 @@ __device__ __forceinline__ bool wait_warp(Shared &sh, uint64_t *bar, uint32_t pa
 template <typename T> struct IsBf16 { static constexpr int v = 0; };
 template <> struct IsBf16<__nv_bfloat16> { static constexpr int v = 1; };
 
+// Joins the n pieces of a pair, by 128 NT threads: with l_p the log2-sums, L =
+// log2 sum 2^l_p and O = sum 2^(l_p - L) O_p, in key order, so the result does
+// not depend on who finishes last.  The weights 2^(l_p - L) of as many rows as
+// fit go to shared memory first; then a thread takes four columns of a row.
+// (Read past L1: other blocks have written the pieces.)
+template <typename T, int D, int NT>
+__device__ __forceinline__ void join_pieces(const PagedArgs &a, const Item &it, int n, int nh,
+                                            int slot0, int tile_pos, int tid, float *w, int w_floats) {
+  constexpr int kQuads = D / 4, kThreads = 128 * NT;
+  const int pg = a.pack, lane = tid & 31;
+  const int positions = min(it.s.lq - it.m0, NT * tile_pos);
+  const int rows = positions * pg, tile_rows = tile_pos * pg;
+  const int64_t step = (int64_t)nh * (NT * kBM);  // rows from a piece to the next
+  // row x of the pair in its slot, and in the output
+  const auto part_row = [&](int x) {
+    const int t = NT == 2 && x >= tile_rows ? 1 : 0;
+    return (int64_t)slot0 * (NT * kBM) + t * kBM + (x - t * tile_rows);
+  };
+  const auto out_row = [&](int x, int &hr) {
+    const int p = x / pg;
+    hr = pg > 1 ? it.head * pg + x - p * pg : it.head;
+    return (int64_t)(it.s.q0 + it.m0 + p);
+  };
+  const int batch = max(1, min(rows, w_floats / n));
+  for (int x0 = 0; x0 < rows; x0 += batch) {
+    const int x1 = min(rows, x0 + batch);
+    // one warp per row, lanes over the pieces; few pieces: several rows a warp
+    int lanes = 32;
+    while (lanes > 1 && lanes / 2 >= n) lanes /= 2;
+    const int sub = lane & (lanes - 1);
+    for (int xb = x0 + (tid - sub) / lanes; xb - (lane - sub) / lanes < x1; xb += kThreads / lanes) {
+      const bool on = xb < x1;
+      const float *l = a.lse_part + (on ? part_row(xb) : 0);
+      float m = -INFINITY, sum = 0.f;
+      if (on)
+        for (int p = sub; p < n; p += lanes) m = fmaxf(m, __ldcg(l + p * step));
+      for (int o = lanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (on)
+        for (int p = sub; p < n; p += lanes) {
+          const float e = m > -INFINITY ? exp2f(__ldcg(l + p * step) - m) : 0.f;
+          w[(xb - x0) * n + p] = e;
+          sum += e;
+        }
+      for (int o = lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      if (on) {
+        for (int p = sub; p < n; p += lanes) w[(xb - x0) * n + p] *= inv;
+        if (sub == 0) {
+          int hr;
+          const int64_t row = out_row(xb, hr);
+          a.lse[(int64_t)hr * a.total_q + row] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+        }
+      }
+    }
+    named_bar_sync(1, kThreads);
+#pragma unroll 2
+    for (int y = tid; y < (x1 - x0) * kQuads; y += kThreads) {
+      const int x = y / kQuads, c = y % kQuads;
+      const float4 *src = reinterpret_cast<const float4 *>(a.o_part + part_row(x0 + x) * D) + c;
+      float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int p = 0; p < n; ++p) {
+        const float wp = w[x * n + p];
+        const float4 v = __ldcg(src + p * step * kQuads);
+        o[0] = fmaf(wp, v.x, o[0]);
+        o[1] = fmaf(wp, v.y, o[1]);
+        o[2] = fmaf(wp, v.z, o[2]);
+        o[3] = fmaf(wp, v.w, o[3]);
+      }
+      int hr;
+      const int64_t row = out_row(x0 + x, hr);
+      store_vec<T, 4>(static_cast<T *>(a.o) + (row * a.hq + hr) * D + c * 4, o);
+    }
+    named_bar_sync(1, kThreads);
+  }
+}
+
 template <typename T, int D, int BN, int NT>
 __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN, NT>::kCtas)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -337,14 +441,54 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pg = a.pack;
-  // the combine kernel may start to find its tiles as soon as there is room
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // shapes of the sequences: every warp but the one that allocates TMEM
+  Shapes shapes{reinterpret_cast<Shape *>(smem), 0.f, 0.f, 0};
+  constexpr int kGather = C::kThreads / 32 - 1;
+  if (warp == 1) {
+    tmem_alloc(&sh.tmem_base, C::kTmemCols);
+    tmem_relinquish();
+  } else {
+    if (threadIdx.x == C::kVWarp * 32) {
+      prefetch_tmap(&tq);
+      prefetch_tmap(&tk);
+      prefetch_tmap(&tv);
+      mbar_init(&sh.q_full, 1);
+      for (int s = 0; s < ST; ++s) {
+        mbar_init(&sh.k_full[s], 1);
+        mbar_init(&sh.k_empty[s], 1);
+        mbar_init(&sh.v_full[s], 1);
+        mbar_init(&sh.v_empty[s], 1);
+      }
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(&sh.s_full[s], 1);
+        mbar_init(&sh.o_done[s], 1);
+        mbar_init(&sh.v_clean[s], 1);
+      }
+      mbar_init(&sh.all_done, 1);
+      sh.wait_ns = a.wait_ns;
+      sh.abort = 0;
+      fence_mbar_init();
+    }
+    const int w = warp == 0 ? 0 : warp - 1;
+    if (w * 32 < a.batch) {
+      const Shapes sum = gather_shapes(a, shapes.at, w, kGather, tile_pos * NT, BN, blockIdx.x == 0);
+      if (lane == 0) sh.sums[w] = sum;
+    }
+  }
+  if (a.batch > 32) __syncthreads();  // (else warp 0 has gathered all)
   Box early{-1, 0};  // the K producer's first boxes, on their way before the others start
   if (warp == 0) {
+    __syncwarp();
+    for (int w = 0; w < kGather && w * 32 < a.batch; ++w) {
+      shapes.work += sh.sums[w].work;
+      shapes.pairs += sh.sums[w].pairs;
+      shapes.longest = max(shapes.longest, sh.sums[w].longest);
+    }
     Item it{};
     it.pieces = 1;
-    const bool found = find_item(a, blockIdx.x, tile_pos * NT, BN, false, blockIdx.x == 0, it);
+    const bool found = find_item(a, shapes, blockIdx.x, tile_pos * NT, BN, it);
     const Piece p = piece_of(a, it, tile_pos * NT, BN, found);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // paged_zero_kernel
     early = fetch_boxes(a, it, p, BN / box_rows, box_rows, p.n_lo * BN, 0);
     if (lane == 0) {
       sh.item = it;
@@ -357,30 +501,9 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
       }
       fence_mbar_init();
     }
-  } else if (warp == 1) {
-    tmem_alloc(&sh.tmem_base, C::kTmemCols);
-    tmem_relinquish();
-  } else if (threadIdx.x == C::kVWarp * 32) {
-    mbar_init(&sh.q_full, 1);
-    for (int s = 0; s < ST; ++s) {
-      mbar_init(&sh.k_full[s], 1);
-      mbar_init(&sh.k_empty[s], 1);
-      mbar_init(&sh.v_full[s], 1);
-      mbar_init(&sh.v_empty[s], 1);
-    }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&sh.s_full[s], 1);
-      mbar_init(&sh.o_done[s], 1);
-      mbar_init(&sh.v_clean[s], 1);
-    }
-    mbar_init(&sh.all_done, 1);
-    sh.wait_ns = a.wait_ns;
-    sh.abort = 0;
-    prefetch_tmap(&tq);
-    prefetch_tmap(&tk);
-    prefetch_tmap(&tv);
-    fence_mbar_init();
   }
+  // (the shapes were where Q lands next)
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -800,6 +923,27 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
         else if (it.slot < a.slots)
           a.lse_part[part] = lse2;
       }
+      if (it.pieces > 1) __threadfence();  // before the piece is counted as written
+    }
+    // The block that writes the last piece of a pair joins them (its softmax
+    // warps, which have the registers for it; every copy and product of the
+    // block has completed, so the tiles' space is free).
+    // (the item is read again from shared memory: registers are short above)
+    if (live && reinterpret_cast<volatile int &>(sh.item.pieces) > 1) {
+      named_bar_sync(1, 128 * NT);
+      const Item jt = sh.item;
+      const int nh = a.pack > 1 ? a.hkv : a.hq, n = sh.piece.written;
+      const int slot0 = jt.slot - jt.piece * nh;  // of the first piece
+      const int tid = threadIdx.x - 32 * C::kSoftmaxWarp0;
+      const bool fits = slot0 + (n - 1) * nh < a.slots;
+      if (tid == 0) {
+        sh.joins = fits && atomicAdd(&a.written[slot0], 1) == n - 1;
+        __threadfence();
+      }
+      named_bar_sync(1, 128 * NT);
+      if (sh.joins)
+        join_pieces<T, D, NT>(a, jt, n, nh, slot0, tile_pos, tid, reinterpret_cast<float *>(smem),
+                              C::kSmemData / 4);
     }
   }
   tc_fence_before();
@@ -807,75 +951,12 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-constexpr int kCombineWarps = 4;
-
-// Joins the pieces of cut rows, one warp per row: with l_p the log2-sums,
-// L = log2 sum 2^l_p and O = sum 2^(l_p - L) O_p, in piece order.  One block per
-// tile, head and row group.
-template <typename T, int D, int BN, int NT>
-__global__ void __launch_bounds__(kCombineWarps * 32)
-    paged_combine_kernel(const PagedArgs a, const int tile_pos) {
-  constexpr int V = D / 32;
-  __shared__ Item item;
-  __shared__ int live;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) {
-    Item it{};
-    it.pieces = 1;
-    const bool found = find_item(a, blockIdx.x, tile_pos * NT, BN, true, false, it);
-    if (lane == 0) {
-      item = it;
-      live = found && it.pieces > 1;
-    }
-  }
-  __syncthreads();
-  // Launched while the blocks of paged_tc_kernel still run: from here on they
-  // have all finished and their results can be read.  Every thread waits, so
-  // that this grid, and with it the call, does not end before that one.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!live) return;
-  const Item it = item;
-  const int pg = a.pack, nh = pg > 1 ? a.hkv : a.hq;
-  const Steps all = key_steps(a, it.s, it.m0, tile_pos * NT, BN);
-  const int per = (all.nt + it.pieces - 1) / it.pieces;
-  const int n = all.nt == 0 ? 1 : (all.nt + per - 1) / per;  // pieces that were written
-  if ((int64_t)it.slot + (int64_t)(n - 1) * nh >= a.slots) return;
-  for (int x = blockIdx.y * kCombineWarps + warp; x < NT * tile_pos * pg;
-       x += gridDim.y * kCombineWarps) {
-    const int t = x / (tile_pos * pg), r = x % (tile_pos * pg);
-    const int i = it.m0 + t * tile_pos + r / pg;
-    if (i >= it.s.lq) break;  // (rows come in order of position)
-    const int hr = pg > 1 ? it.head * pg + r % pg : it.head;
-    const int64_t step = (int64_t)nh * (NT * kBM);  // rows from a piece to the next
-    const int64_t row0 = (int64_t)it.slot * (NT * kBM) + t * kBM + r;
-    float m = -INFINITY;
-    for (int p = lane; p < n; p += 32) m = fmaxf(m, a.lse_part[row0 + p * step]);
-    m = warp_max(m);
-    float acc[V], sum = 0.f;
-#pragma unroll
-    for (int u = 0; u < V; ++u) acc[u] = 0.f;
-    if (m > -INFINITY) {
-      for (int p0 = 0; p0 < n; p0 += 32) {
-        const float w_mine =
-            p0 + lane < n ? exp2f(a.lse_part[row0 + (p0 + lane) * step] - m) : 0.f;
-        sum += warp_sum(w_mine);
-        const int k = min(32, n - p0);
-#pragma unroll 4
-        for (int p = 0; p < k; ++p) {
-          const float w = __shfl_sync(0xffffffffu, w_mine, p);
-          const float *src = a.o_part + (row0 + (p0 + p) * step) * D + lane * V;
-#pragma unroll
-          for (int u = 0; u < V; ++u) acc[u] = fmaf(w, src[u], acc[u]);
-        }
-      }
-    }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-    for (int u = 0; u < V; ++u) acc[u] *= inv;
-    store_vec<T, V>(static_cast<T *>(a.o) + ((int64_t)(it.s.q0 + i) * a.hq + hr) * D + lane * V, acc);
-    if (lane == 0)
-      a.lse[(int64_t)hr * a.total_q + it.s.q0 + i] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
-  }
+// Clears the counts of written pieces.  The main kernel starts beside it (its
+// blocks wait for this grid only where they are about to hand out work), which
+// costs a call 1 us; a memset before it cost 3.
+__global__ void paged_zero_kernel(int *written, int n) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int i = threadIdx.x; i < n; i += blockDim.x) written[i] = 0;
 }
 
 // (page, slot, head, D) pool, box {64, 1, box_rows, 1}, 128-byte swizzle.
@@ -914,30 +995,30 @@ cudaError_t paged(const PagedArgs &a, const PagedPlan &plan, cudaStream_t st) {
             "boxes of %d, pack=%d, num_splits=%d (wave %d), grid=%lld x %d threads, smem=%d B",
             D, NT, BN, box_rows, a.pack, a.num_splits, a.wave, (long long)plan.items, C::kThreads,
             C::kSmem);
-  paged_tc_kernel<T, D, BN, NT><<<(unsigned)plan.items, C::kThreads, C::kSmem, st>>>(
-      tq, tk, tv, a, plan.tile_pos, box_rows);
-  count_launches(1);
-  if (a.num_splits != 1) {
-    const int64_t rows = std::max<int64_t>(1, (int64_t)a.total_q * a.pack / a.batch);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)plan.tiles, (unsigned)std::min<int64_t>(NT * 8, (rows + 15) / 16));
-    cfg.blockDim = dim3(kCombineWarps * 32);
-    cfg.stream = st;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, paged_combine_kernel<T, D, BN, NT>, a, plan.tile_pos);
-    if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)plan.items);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  if (plan.slots > 0) {
+    paged_zero_kernel<<<1, 1024, 0, st>>>(a.written, (int)plan.slots);
     count_launches(1);
+    cfg.numAttrs = 1;
   }
+  e = cudaLaunchKernelEx(&cfg, paged_tc_kernel<T, D, BN, NT>, tq, tk, tv, a, plan.tile_pos, box_rows);
+  if (e != cudaSuccess) return e;
+  count_launches(1);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-PagedPlan paged_plan(int batch, int total_q, int hq, int hkv, int d, int num_splits, int sms) {
+PagedPlan paged_plan(int batch, int total_q, int hq, int hkv, int d, int num_splits, int64_t keys,
+                     int sms) {
   PagedPlan p{};
   const int g = hq / hkv;
   // The g query heads of a KV head share tiles: K and V are then read once for
@@ -955,7 +1036,7 @@ PagedPlan paged_plan(int batch, int total_q, int hq, int hkv, int d, int num_spl
   const int64_t wave = (int64_t)sms * (p.layout == 1 && d <= 128 ? 2 : 1);
   // sum of ceil(n_i / pos) over sequences of sum total_q
   p.tiles = (total_q / pos + std::min(batch, total_q)) * (int64_t)nh;
-  p.num_splits = num_splits;
+  p.num_splits = std::min(num_splits, kMaxSplits);
   // enough tiles for several waves even if no sequence leaves one half empty
   if (num_splits == 0 && (int64_t)(total_q + pos - 1) / pos * nh >= 4 * wave) p.num_splits = 1;
   p.wave = (int)wave;
@@ -969,11 +1050,15 @@ PagedPlan paged_plan(int batch, int total_q, int hq, int hkv, int d, int num_spl
     // ones and one more per pair; of cut pairs at most twice as many as full ones
     if (p.max_waves == 3) p.items = std::max(p.items, p.tiles + 2 * wave);
     p.slots = std::min(4 * wave, p.items);
+    // short caches: a pair cannot make more pieces than this
+    const int64_t steps = keys / (p.layout == 2 ? 128 : 64) + 2;
+    p.items = std::min(p.items, p.tiles * ((steps + kMinPieceSteps - 1) / kMinPieceSteps));
   } else {
     p.items = p.tiles * p.num_splits;
     p.slots = p.num_splits > 1 ? p.items : 0;
   }
-  p.ws_bytes = (size_t)p.slots * kBM * p.layout * (d + 1) * sizeof(float);
+  // partial O and log2-sums, and a count of written pieces per slot
+  p.ws_bytes = (size_t)p.slots * (kBM * p.layout * (d + 1) * sizeof(float) + sizeof(int));
   return p;
 }
 

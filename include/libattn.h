@@ -279,7 +279,8 @@ attn_status attn_fwd_kvcache_noalloc(const void *q, void *k_cache, void *v_cache
  *
  * q_row_stride: elements between consecutive query rows (0: hq * d), at least
  * hq * d and a multiple of 8.  num_splits: 0 = choose on the device from the
- * lengths; else the number of key ranges each row's keys are split into.  The
+ * lengths; else the number of key ranges each row's keys are split into (1024
+ * at most; larger numbers count as that).  The
  * result does not depend on it beyond rounding.  workspace: at least
  * attn_fwd_paged_workspace_size(...) bytes, 256-byte aligned, contents
  * arbitrary; calls that may run at the same time need one each.
