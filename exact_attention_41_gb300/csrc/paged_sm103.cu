@@ -424,7 +424,9 @@ __device__ __forceinline__ void join_pieces(const PagedArgs &a, const Item &it, 
   }
 }
 
-template <typename T, int D, int BN, int NT>
+// kCut: keys may be cut into pieces.  (The code that joins them costs the two-tile
+// layout 1.5% in registers of its loop, whether or not it runs.)
+template <typename T, int D, int BN, int NT, bool kCut>
 __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN, NT>::kCtas)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                     const __grid_constant__ CUtensorMap tv, const PagedArgs a, const int tile_pos,
@@ -923,13 +925,13 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
         else if (it.slot < a.slots)
           a.lse_part[part] = lse2;
       }
-      if (it.pieces > 1) __threadfence();  // before the piece is counted as written
+      if (kCut && it.pieces > 1) __threadfence();  // before the piece is counted as written
     }
     // The block that writes the last piece of a pair joins them (its softmax
     // warps, which have the registers for it; every copy and product of the
     // block has completed, so the tiles' space is free).
     // (the item is read again from shared memory: registers are short above)
-    if (live && reinterpret_cast<volatile int &>(sh.item.pieces) > 1) {
+    if (kCut && live && reinterpret_cast<volatile int &>(sh.item.pieces) > 1) {
       named_bar_sync(1, 128 * NT);
       const Item jt = sh.item;
       const int nh = a.pack > 1 ? a.hkv : a.hq, n = sh.piece.written;
@@ -977,7 +979,7 @@ bool make_pool_map(CUtensorMap *m, const void *base, const PagedArgs &a, int64_t
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int D, int BN, int NT>
+template <typename T, int D, int BN, int NT, bool kCut = true>
 cudaError_t paged(const PagedArgs &a, const PagedPlan &plan, cudaStream_t st) {
   using C = PagedCfg<D, BN, NT>;
   // a box never leaves its page
@@ -987,9 +989,9 @@ cudaError_t paged(const PagedArgs &a, const PagedPlan &plan, cudaStream_t st) {
       !make_pool_map(&tk, a.k_cache, a, a.k_ps, box_rows) ||
       !make_pool_map(&tv, a.v_cache, a, a.v_ps, box_rows))
     return cudaErrorInvalidValue;
-  cudaError_t e = set_smem_once<paged_tc_kernel<T, D, BN, NT>>(C::kSmem);
+  cudaError_t e = set_smem_once<paged_tc_kernel<T, D, BN, NT, kCut>>(C::kSmem);
   if (e == cudaSuccess && NT == 2)  // 128 * 88 + 256 * 208 after setmaxnreg
-    e = check_regs_once<paged_tc_kernel<T, D, BN, NT>>(C::kThreads, 128 * 88 + 256 * 208);
+    e = check_regs_once<paged_tc_kernel<T, D, BN, NT, kCut>>(C::kThreads, 128 * 88 + 256 * 208);
   if (e != cudaSuccess) return e;
   debug_log("paged: paged_tc_kernel d=%d, %d query tile(s) of 128 rows per block, %d-key tiles in "
             "boxes of %d, pack=%d, num_splits=%d (wave %d), grid=%lld x %d threads, smem=%d B",
@@ -1009,7 +1011,7 @@ cudaError_t paged(const PagedArgs &a, const PagedPlan &plan, cudaStream_t st) {
     count_launches(1);
     cfg.numAttrs = 1;
   }
-  e = cudaLaunchKernelEx(&cfg, paged_tc_kernel<T, D, BN, NT>, tq, tk, tv, a, plan.tile_pos, box_rows);
+  e = cudaLaunchKernelEx(&cfg, paged_tc_kernel<T, D, BN, NT, kCut>, tq, tk, tv, a, plan.tile_pos, box_rows);
   if (e != cudaSuccess) return e;
   count_launches(1);
   return cudaGetLastError();
@@ -1068,6 +1070,9 @@ cudaError_t launch_paged_tc(const PagedArgs &a, const PagedPlan &plan, cudaStrea
     case 64:
       return bf ? paged<__nv_bfloat16, 64, 64, 1>(a, plan, st) : paged<__half, 64, 64, 1>(a, plan, st);
     case 128:
+      if (plan.layout == 2 && plan.num_splits == 1)
+        return bf ? paged<__nv_bfloat16, 128, 128, 2, false>(a, plan, st)
+                  : paged<__half, 128, 128, 2, false>(a, plan, st);
       if (plan.layout == 2)
         return bf ? paged<__nv_bfloat16, 128, 128, 2>(a, plan, st) : paged<__half, 128, 128, 2>(a, plan, st);
       return bf ? paged<__nv_bfloat16, 128, 64, 1>(a, plan, st) : paged<__half, 128, 64, 1>(a, plan, st);
