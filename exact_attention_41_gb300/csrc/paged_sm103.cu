@@ -899,7 +899,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
 #pragma unroll
           for (int e = 0; e < 64; ++e) u[e] = 0u;
         }
-        if (it.pieces == 1) {
+        if (!kCut || it.pieces == 1) {
           uint32_t w[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e)
@@ -910,7 +910,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
             for (int e = 0; e < 8; ++e)
               dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
           }
-        } else if (valid && it.slot < a.slots) {
+        } else if (kCut && valid && it.slot < a.slots) {
           float4 *dst = reinterpret_cast<float4 *>(a.o_part + part * D + c2 * 64);
 #pragma unroll
           for (int e = 0; e < 16; ++e)
@@ -920,7 +920,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
         }
       }
       if (valid) {
-        if (it.pieces == 1)
+        if (!kCut || it.pieces == 1)
           a.lse[(int64_t)hr * a.total_q + sq.q0 + i] = lse2 * kLn2;
         else if (it.slot < a.slots)
           a.lse_part[part] = lse2;
