@@ -1,0 +1,292 @@
+"""The norm with rotation, the append and the paged-chunk attention as they are
+used together: a prompt and decode steps against a growing cache, the same
+captured in CUDA graphs, calls on two streams at once, a training step through
+the dense attention; and the places where such calls go wrong (many sequences,
+shared pages, caches past 2^31 elements)."""
+import math
+
+import numpy as np
+import pytest
+
+from exact_attention_41_gb300 import synthetic as syn
+from oracle import attention as ref
+from oracle import serving
+from tests.helpers import assert_close, assert_lse, dev, dev_i32, f64, host
+from tests.test_paged_parity import call, check, make, run
+
+pytestmark = pytest.mark.gpu
+
+
+def freqs(rot, base=10000.0):
+    return base ** (-2.0 * np.arange(rot // 2) / rot)
+
+
+class Layer:
+    """A cache of three sequences, the weights of one layer's norms, and one step
+    of it on the device and in the oracle (which takes the rounded q, k, v that
+    the device's own append made, so that only the attention's error counts)."""
+
+    def __init__(self, seed, page=16, hq=8, hkv=2, d=64, dtype=syn.BF16, pages=60):
+        from exact_attention_41_gb300 import libattn
+        import torch
+
+        self.rng = np.random.default_rng(seed)
+        self.hq, self.hkv, self.d, self.dtype, self.page = hq, hkv, d, dtype, page
+        self.kc = torch.zeros(pages, page, hkv, d, device="cuda", dtype=torch.bfloat16)
+        self.vc = torch.zeros_like(self.kc)
+        self.table_host = self.rng.permutation(pages).reshape(3, -1).astype(np.int32)
+        self.table = dev_i32(self.table_host)
+        self.lens = dev_i32([0, 0, 0])
+        self.phases = libattn.rope_phases(freqs(d))
+        bits = [syn.round_bits((1 + 0.2 * self.rng.standard_normal(d)).astype(np.float32), dtype)
+                for _ in range(2)]
+        self.wq, self.wk = (dev(b, dtype) for b in bits)
+        self.w64 = [f64(b, dtype) for b in bits]
+
+    def inputs(self, total):
+        mk = lambda h: syn.normal_bits(self.rng, (total, h, self.d), self.dtype)
+        return mk(self.hq), mk(self.hkv), mk(self.hkv)
+
+    def step(self, q, k, v, cu, **kw):
+        from exact_attention_41_gb300 import libattn
+
+        qr = libattn.kvcache_append(k, v, self.kc, self.vc, cu, self.lens, block_table=self.table,
+                                    q=q, phases=self.phases, q_weight=self.wq, k_weight=self.wk)
+        return libattn.fwd_paged(qr, self.kc, self.vc, cu, self.lens, block_table=self.table,
+                                 causal=True, **kw)
+
+
+def test_prompt_then_decode_against_the_oracle():
+    """A ragged prompt, then a drafted step, then single tokens: every step equals
+    dense causal attention over all tokens so far, normed and rotated at their
+    positions by the oracle."""
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    ly = Layer(31)
+    ks = [np.zeros((0, ly.hkv, ly.d)) for _ in range(3)]
+    vs = [np.zeros((0, ly.hkv, ly.d)) for _ in range(3)]
+    for new in ([37, 1, 90], [4, 4, 1], [1, 1, 1], [1, 0, 1]):
+        cu = np.cumsum([0] + new).astype(np.int32)
+        q, k, v = ly.inputs(int(cu[-1]))
+        o, lse = ly.step(dev(q, ly.dtype), dev(k, ly.dtype), dev(v, ly.dtype), dev_i32(cu))
+        torch.cuda.synchronize()
+        for i, n in enumerate(new):
+            if n == 0:
+                continue
+            rows = slice(cu[i], cu[i + 1])
+            pos = len(ks[i]) + np.arange(n)
+            args = (pos, freqs(ly.d))
+            qi = serving.norm_rope(f64(q[rows], ly.dtype), *args, ly.w64[0])
+            ks[i] = np.concatenate([ks[i], serving.norm_rope(f64(k[rows], ly.dtype), *args, ly.w64[1])])
+            vs[i] = np.concatenate([vs[i], f64(v[rows], ly.dtype)])
+            # (the oracle keeps q and k unrounded: their bf16 rounding moves a
+            # score by 2^-8 sqrt(2) |s| / sqrt(d) and the sums over keys below the
+            # contract's tolerance)
+            ro, rl = ref.forward(qi[None], ks[i][None], vs[i][None], 1 / math.sqrt(ly.d), causal=True)
+            assert_close(host(o)[rows], ro[0], ly.dtype, f"sequence {i}")
+            np.testing.assert_allclose(host(lse)[:, rows], rl[0], atol=2e-2)
+        ly.lens += dev_i32(new)
+    assert libattn.device_error() == (0, 0)
+
+
+def test_decode_step_in_a_graph_with_growing_lengths():
+    """One captured step (append, attention, advance) replayed while the lengths
+    grow on the device: the bits of the same steps run eagerly; a second graph
+    that shares the workspace, replayed in turn with the first, too."""
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    ly, twin = Layer(32, pages=300), Layer(32, pages=300)
+    cu = dev_i32([0, 1, 2, 3])
+    prompt = [200, 1, 777]
+    pcu = np.cumsum([0] + prompt).astype(np.int32)
+    q, k, v = ly.inputs(int(pcu[-1]))
+    for l in (ly, twin):
+        l.step(*(dev(x, l.dtype) for x in (q, k, v)), dev_i32(pcu))
+        l.lens += dev_i32(prompt)
+    steps = [ly.inputs(3) for _ in range(6)]
+    bufs = [dev(x, ly.dtype) for x in steps[0]]
+    ws = libattn.paged_workspace(bufs[0], ly.kc, 3)
+    outs = [torch.empty_like(bufs[0]) for _ in range(2)]
+
+    def one(out):
+        ly.step(*bufs, cu, workspace=ws, out=out)
+        libattn.kvcache_advance(ly.lens, 1)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        keep = [t.clone() for t in (ly.kc, ly.vc, ly.lens)]
+        one(outs[0])
+        for t, c in zip((ly.kc, ly.vc, ly.lens), keep):
+            t.copy_(c)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = []
+    for out in outs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            one(out)
+        graphs.append(g)
+    for i, x in enumerate(steps):
+        for b, s in zip(bufs, x):
+            b.copy_(dev(s, ly.dtype))
+        graphs[i % 2].replay()
+        o, _ = twin.step(*(dev(s, ly.dtype) for s in x), cu)
+        libattn.kvcache_advance(twin.lens, 1)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i % 2], o), i
+    assert torch.equal(ly.lens, twin.lens) and torch.equal(ly.kc, twin.kc)
+
+
+def test_two_calls_at_once_on_two_streams():
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    cases = [make(41, [1, 5, 40], [3000, 100, 900], 8, 2, 128, 16, syn.BF16),
+             make(42, [300, 2], [1000, 4000], 8, 2, 128, 32, syn.BF16)]
+    want = [call(c, causal=True) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    args = [(dev(c["q"], c["dtype"]), dev(c["kc"], c["dtype"]), dev(c["vc"], c["dtype"]),
+             dev_i32(c["cu"]), dev_i32(c["cached"]), dev_i32(c["table"])) for c in cases]
+    spaces = [libattn.paged_workspace(a[0], a[1], 3) for a in args]
+    got = [[None, None] for _ in range(10)]
+    torch.cuda.synchronize()
+    for r in range(10):
+        for j, (st, a) in enumerate(zip(streams, args)):
+            with torch.cuda.stream(st):
+                got[r][j] = libattn.fwd_paged(*a[:5], block_table=a[5], causal=True,
+                                              workspace=spaces[j])
+    torch.cuda.synchronize()
+    for g in got:
+        for j in range(2):
+            assert torch.equal(g[j][0], want[j][0]) and torch.equal(g[j][1], want[j][1])
+
+
+def test_training_step_through_the_dense_attention():
+    """qkv -> norm and rotation -> attention -> and back, gradients of the packed
+    projection and both weights against the oracle's chain; then the same step
+    captured in a graph while the eager tensors live."""
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    b, s, h, d, dtype = 2, 150, 4, 64, syn.F16
+    rng = np.random.default_rng(51)
+    qkv_bits = syn.normal_bits(rng, (b, s, 3, h, d), dtype)
+    do_bits = syn.normal_bits(rng, (b, s, h, d), dtype)
+    w = [syn.round_bits((1 + 0.2 * rng.standard_normal(d)).astype(np.float32), dtype) for _ in range(2)]
+    kw = dict(phases=libattn.rope_phases(freqs(d)), q_weight=dev(w[0], dtype), k_weight=dev(w[1], dtype))
+    qkv, do = dev(qkv_bits, dtype), dev(do_bits, dtype)
+    bufs = [torch.empty(b, s, h, d, device="cuda", dtype=torch.float16) for _ in range(2)]
+    dqkv = torch.empty_like(qkv)
+
+    def step():
+        q, k = libattn.qk_norm_rope(qkv[:, :, 0], qkv[:, :, 1], q_out=bufs[0], k_out=bufs[1], **kw)
+        o, lse = libattn.fwd(q, k, qkv[:, :, 2], causal=True)
+        dq, dk, dv = libattn.bwd(q, k, qkv[:, :, 2], o, lse, do, causal=True, deterministic=True)
+        _, _, dwq, dwk = libattn.qk_norm_rope_bwd(qkv[:, :, 0], qkv[:, :, 1], dq, dk,
+                                                  dq=dqkv[:, :, 0], dk=dqkv[:, :, 1], **kw)
+        dqkv[:, :, 2] = dv
+        return dqkv, dwq, dwk
+
+    got = [t.clone() for t in step()]
+    torch.cuda.synchronize()
+    x = f64(qkv_bits, dtype)
+    pos = np.tile(np.arange(s), b)
+    w64 = [f64(t, dtype) for t in w]
+    turned = [serving.norm_rope(x[:, :, i].reshape(-1, h, d), pos, freqs(d), w64[i]).reshape(b, s, h, d)
+              for i in range(2)]
+    grads = ref.backward(turned[0], turned[1], x[:, :, 2], f64(do_bits, dtype), 1 / math.sqrt(d), True)
+    for i in range(2):
+        gx, gw = serving.norm_rope_backward(x[:, :, i].reshape(-1, h, d), grads[i].reshape(-1, h, d),
+                                            pos, freqs(d), w64[i])
+        # rounding of q, k (2^-11 relative) and of dq, dk between the calls: the
+        # contract's tolerance, at the size of the gradients here (up to 8)
+        np.testing.assert_allclose(host(got[0])[:, :, i], gx.reshape(b, s, h, d), atol=1.5e-2, rtol=1e-2)
+        scale = np.abs(gw).max()
+        np.testing.assert_allclose(host(got[1 + i]), gw, atol=5e-3 * scale + 2e-2, rtol=5e-3)
+    assert_close(host(got[0])[:, :, 2], grads[2], dtype, "dv")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    dqkv.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    for a, c in zip(out, got):
+        assert torch.equal(a, c)
+
+
+def test_pages_shared_by_sequences():
+    """A common prefix: two sequences' tables hold the same pages."""
+    c = make(61, [3, 3, 1], [100, 100, 40], 8, 2, 64, 16, syn.BF16, poison=False)
+    c["table"][1, :6] = c["table"][0, :6]
+    run(c, causal=True)
+
+
+def test_more_sequences_than_the_first_group_are_checked():
+    """The 36th of 40 sequences has a negative length: flagged, its rows empty."""
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    c = make(62, [1] * 40, [50] * 40, 4, 1, 64, 16, syn.F16, poison=False)
+    c["cached"][35] = -9
+    libattn.device_error()
+    for splits in (0, 1):
+        o, lse = call(c, causal=True, num_splits=splits)
+        torch.cuda.synchronize()
+        st, word = libattn.device_error()
+        assert st == 6 and word == 16
+        assert (host(o)[35] == 0).all() and np.isneginf(host(lse)[:, 35]).all()
+        assert np.isfinite(host(lse)[:, :35]).all()
+
+
+def test_thousands_of_sequences():
+    """More sequences than the block keeps in shared memory."""
+    rng = np.random.default_rng(63)
+    new = [int(x) for x in rng.choice([0, 1, 1, 2], 5000)]
+    cached = [int(x) for x in rng.integers(0, 40, 5000)]
+    c = make(63, new, cached, 2, 1, 64, 16, syn.BF16)
+    run(c, causal=True)
+
+
+@pytest.mark.parametrize("page", [16, 256, 24])
+def test_cache_past_2_31_elements(page):
+    """A pool of 2.3e9 elements, one sequence at its start and one at its end:
+    append, then attention over both."""
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    hq, hkv, d, dtype = 8, 8, 128, syn.BF16
+    pages = 2_300_000_000 // (page * hkv * d)
+    kc = torch.empty(pages, page, hkv, d, device="cuda", dtype=torch.bfloat16)
+    vc = torch.empty_like(kc)
+    rng = np.random.default_rng(64)
+    new = [150, 70]
+    cu = np.cumsum([0] + new).astype(np.int32)
+    need = [-(-n // page) for n in new]
+    table = np.full((2, max(need)), -1, np.int32)
+    table[0, :need[0]] = np.arange(need[0])
+    table[1, :need[1]] = pages - 1 - np.arange(need[1])
+    q, k, v = (syn.normal_bits(rng, (sum(new), h, d), dtype) for h in (hq, hkv, hkv))
+    zero = dev_i32([0, 0])
+    args = (dev_i32(cu), zero)
+    libattn.kvcache_append(dev(k, dtype), dev(v, dtype), kc, vc, *args, block_table=dev_i32(table))
+    o, lse = libattn.fwd_paged(dev(q, dtype), kc, vc, *args, block_table=dev_i32(table), causal=True)
+    torch.cuda.synchronize()
+    assert libattn.device_error() == (0, 0)
+    ro, rl = ref.varlen_forward(f64(q, dtype), f64(k, dtype), f64(v, dtype), cu, cu,
+                                1 / math.sqrt(d), True)
+    assert_close(host(o), ro, dtype, "out")
+    assert_lse(host(lse), rl)
