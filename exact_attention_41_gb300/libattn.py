@@ -121,10 +121,10 @@ def _torch():
 
 def _dt(t) -> int:
     torch = _torch()
-    if t.dtype == torch.float16:
-        return F16
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return BF16
+    if t.dtype is torch.float16:
+        return F16
     raise TypeError(f"dtype {t.dtype} is not fp16/bf16")
 
 
@@ -430,33 +430,39 @@ def fwd_fp8(q, k, v, descale_q=1.0, descale_k=1.0, descale_v=1.0, *, scale=None,
 # (The checks below are written out, with their messages made only when they
 # fail: on small calls the host's time is the call's time.)
 
-def _call(name, args, ts):
-    """Makes the call `name` with `args` and, last, the current stream of the one
-    CUDA device that the tensors ts (None: absent) lie on."""
+def _call(fn, args, dense, strided=()):
+    """Makes the call fn (of lib()) with `args` and, last, the current stream of
+    the one CUDA device that the tensors lie on (None: absent; dense ones have to
+    be contiguous)."""
     index = None
-    for t in ts:
+    for t in dense:
         if t is not None:
             i = t.get_device()
             if i != index:
-                if i < 0:
-                    raise ValueError("tensors must be on a CUDA device")
-                if index is not None:
-                    raise ValueError("tensors must be on one device")
-                index = i
-    cuda = _torch().cuda
+                index = _same_device(index, i)
+            if not t.is_contiguous():
+                raise ValueError("tensors must be contiguous")
+    for t in strided:
+        if t is not None:
+            i = t.get_device()
+            if i != index:
+                index = _same_device(index, i)
+    cuda = _torch_module.cuda
     if index == cuda.current_device():
-        st = getattr(lib(), name)(*args, _stream())
+        st = fn(*args, _stream())
     else:
         with cuda.device(index):
-            st = getattr(lib(), name)(*args, _stream())
+            st = fn(*args, _stream())
     if st != 0:
-        raise AttnError(st, name)
+        raise AttnError(st, fn.__name__)
 
 
-def _contig(*ts):
-    for t in ts:
-        if t is not None and not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
+def _same_device(index, i):
+    if i < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    if index is not None:
+        raise ValueError("tensors must be on one device")
+    return i
 
 
 def _like(t, ref, shape, what):
@@ -504,7 +510,6 @@ def _cache_args(k_cache, v_cache, cu_seqlens, cache_seqlens, block_table):
         if block_table.dtype != i32 or block_table.dim() != 2 or block_table.shape[0] != batch:
             raise ValueError("block_table must be int32 (batch, max_pages)")
         max_pages = block_table.shape[1]
-    _contig(cu_seqlens, cache_seqlens, block_table)
     return batch, num_pages, page_size, max_pages
 
 
@@ -543,15 +548,16 @@ def fwd_paged(q, k_cache, v_cache, cu_seqlens_q, cache_seqlens, *, block_table=N
         raise ValueError("lse must be (hq, Tq) fp32")
     if workspace is None:
         workspace = paged_workspace(q, k_cache, batch, num_splits)
-    _contig(out, lse, workspace)
     wl, wr = window
-    _call("attn_fwd_paged",
-          (_p(q), _p(k_cache), _p(v_cache), _p(out), _p(lse), _packed_stride(q),
-           _page_stride(k_cache), _page_stride(v_cache), _p(cu_seqlens_q), _p(cache_seqlens),
-           _p(block_table), num_pages, page_size, max_pages, 1 if appended else 0, batch, rows,
-           _dt(q), hq, hkv, d, _scale(scale, d), 1 if causal else 0, int(wl), int(wr), softcap,
-           num_splits, _p(workspace), workspace.nbytes),
-          (q, k_cache, v_cache, cu_seqlens_q, cache_seqlens, block_table, out, lse, workspace))
+    _call(lib().attn_fwd_paged,
+          (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(),
+           _packed_stride(q), _page_stride(k_cache), _page_stride(v_cache),
+           cu_seqlens_q.data_ptr(), cache_seqlens.data_ptr(), _p(block_table), num_pages,
+           page_size, max_pages, 1 if appended else 0, batch, rows, _dt(q), hq, hkv, d,
+           d ** -0.5 if scale is None else scale, 1 if causal else 0, int(wl), int(wr), softcap,
+           num_splits, workspace.data_ptr(), workspace.nbytes),
+          (out, lse, cu_seqlens_q, cache_seqlens, block_table, workspace),
+          (q, k_cache, v_cache))
     return out, lse
 
 
@@ -586,7 +592,6 @@ def _rope_args(phases, q_weight, k_weight, ref):
         _like(q_weight, ref, (d,), "q_weight")
     if k_weight is not None:
         _like(k_weight, ref, (d,), "k_weight")
-    _contig(phases, q_weight, k_weight)
     return rot
 
 
@@ -612,7 +617,6 @@ def _positions(positions, b, s):
         return None
     if positions.dtype != _torch().int32 or positions.numel() != b * s:
         raise ValueError("positions must be int32 with one entry per token")
-    _contig(positions)
     return positions.data_ptr()
 
 
@@ -636,11 +640,11 @@ def qk_norm_rope(q, k, *, phases=None, positions=None, interleaved=False, q_weig
     ref, b, s, hq, hkv, d = _qk_sizes(q, k)
     rot = _rope_args(phases, q_weight, k_weight, ref)
     q_out, k_out = _result(q_out, q, "q_out"), _result(k_out, k, "k_out")
-    _call("attn_qk_norm_rope",
+    _call(lib().attn_qk_norm_rope,
           (_p(q), _p(k), _p(q_out), _p(k_out), _row_stride(q), _row_stride(k),
            _row_stride(q_out), _row_stride(k_out), _p(q_weight), _p(k_weight), eps, _p(phases),
            rot, 1 if interleaved else 0, _positions(positions, b, s), _dt(ref), b, s, hq, hkv, d),
-          (q, k, q_out, k_out, phases, positions, q_weight, k_weight))
+          (phases, positions, q_weight, k_weight), (q, k, q_out, k_out))
     return q_out, k_out
 
 
@@ -673,15 +677,14 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, *, phases=None, positions=None, inter
     dk_weight = _result(dk_weight, None if k is None else k_weight, "dk_weight")
     if workspace is None:
         workspace = qk_norm_rope_bwd_workspace(q, k)
-    _contig(dq_out, dk_out, dq_weight, dk_weight, workspace)
-    _call("attn_qk_norm_rope_bwd",
+    _call(lib().attn_qk_norm_rope_bwd,
           (_p(q), _p(k), _p(dq_out), _p(dk_out), _p(dq), _p(dk), _row_stride(q), _row_stride(k),
            _row_stride(dq), _row_stride(dk), _p(q_weight), _p(k_weight), _p(dq_weight),
            _p(dk_weight), eps, _p(phases), rot, 1 if interleaved else 0,
-           _positions(positions, b, s), _dt(ref), b, s, hq, hkv, d, _p(workspace),
+           _positions(positions, b, s), _dt(ref), b, s, hq, hkv, d, workspace.data_ptr(),
            workspace.nbytes),
-          (q, k, dq_out, dk_out, dq, dk, phases, positions, q_weight, k_weight, dq_weight,
-           dk_weight, workspace))
+          (dq_out, dk_out, phases, positions, q_weight, k_weight, dq_weight, dk_weight, workspace),
+          (q, k, dq, dk))
     return dq, dk, dq_weight, dk_weight
 
 
@@ -705,14 +708,14 @@ def kvcache_append(k_new, v_new, k_cache, v_cache, cu_seqlens, cache_seqlens, *,
         hq = q.shape[1]
         _like(q, k_new, (total, hq, d), "q")
         q_out = _result(q_out, q, "q_out")
-        _contig(q_out)
     rot = _rope_args(phases, q_weight, k_weight, k_new)
-    _call("attn_kvcache_append",
-          (_p(q), _p(q_out), _p(k_new), _p(v_new), _packed_stride(q), _packed_stride(k_new),
-           _packed_stride(v_new), _p(k_cache), _p(v_cache), _page_stride(k_cache),
-           _page_stride(v_cache), _p(cu_seqlens), _p(cache_seqlens), _p(block_table), num_pages,
-           page_size, max_pages, _p(q_weight), _p(k_weight), eps, _p(phases), rot,
-           1 if interleaved else 0, _dt(k_new), batch, total, hq, hkv, d),
-          (k_new, v_new, k_cache, v_cache, cu_seqlens, cache_seqlens, block_table, q, q_out, phases,
-           q_weight, k_weight))
+    _call(lib().attn_kvcache_append,
+          (_p(q), _p(q_out), k_new.data_ptr(), v_new.data_ptr(), _packed_stride(q),
+           _packed_stride(k_new), _packed_stride(v_new), k_cache.data_ptr(), v_cache.data_ptr(),
+           _page_stride(k_cache), _page_stride(v_cache), cu_seqlens.data_ptr(),
+           cache_seqlens.data_ptr(), _p(block_table), num_pages, page_size, max_pages,
+           _p(q_weight), _p(k_weight), eps, _p(phases), rot, 1 if interleaved else 0, _dt(k_new),
+           batch, total, hq, hkv, d),
+          (cu_seqlens, cache_seqlens, block_table, q_out, phases, q_weight, k_weight),
+          (k_new, v_new, k_cache, v_cache, q))
     return q_out
