@@ -78,7 +78,9 @@ struct PagedCfg {
 
 // One unit of work.
 struct Item {
-  int seq, m0, head, piece, pieces, slot;  // m0: first query position
+  int seq, m0, head;  // m0: first query position
+  int piece, pieces;
+  int slot, stride;   // its partial result; from a piece's slot to the next one's
   PagedSeq s;
 };
 
@@ -122,17 +124,18 @@ __device__ __forceinline__ Shape shape_of(const PagedArgs &a, const PagedSeq &s,
 // The shapes of all sequences, in shared memory for the first kMaxShapes (the
 // tiles' own space, which no copy uses yet), and sums over all of them.
 constexpr int kMaxShapes = 4096;
-constexpr int kMaxSplits = 1024;  // their weights have to fit shared memory
+constexpr int kMaxSplits = 1024;
 struct Shapes {
   Shape *at;
   float work, pairs;  // per head: key steps; tiles
+  float long_pairs;   // those of sequences of several tiles
   int longest;        // steps
 };
 // One warp's share, sequences `warp` * 32 + lane and on by `warps` * 32; returns
 // its part of the sums.  raise: report bad lengths.
 __device__ __forceinline__ Shapes gather_shapes(const PagedArgs &a, Shape *at, int warp, int warps,
                                                 int pos, int bn, bool raise) {
-  float work = 0.f, pairs = 0.f;
+  float work = 0.f, pairs = 0.f, long_pairs = 0.f;
   int longest = 0;
   for (int i = warp * 32 + (threadIdx.x & 31); i < a.batch; i += warps * 32) {
     const PagedSeq s = paged_seq(a, i);
@@ -141,9 +144,20 @@ __device__ __forceinline__ Shapes gather_shapes(const PagedArgs &a, Shape *at, i
     if (i < kMaxShapes) at[i] = x;
     work += (float)x.tiles * (float)x.steps;
     pairs += (float)x.tiles;
+    if (x.tiles > 1) long_pairs += (float)x.tiles;
     longest = max(longest, x.steps);
   }
-  return Shapes{at, warp_sum(work), warp_sum(pairs), __reduce_max_sync(0xffffffffu, longest)};
+  return Shapes{at, warp_sum(work), warp_sum(pairs), warp_sum(long_pairs),
+                __reduce_max_sync(0xffffffffu, longest)};
+}
+
+// x / y for x < 2^24 or so, y > 0 alike in the whole grid: a reciprocal and a
+// correction instead of a division's 35 instructions.
+__device__ __forceinline__ int div_up(int x, int y, float inv_y) {
+  int q = (int)((float)x * inv_y);
+  q += q * y < x;
+  q += q * y < x;
+  return q - ((q - 1) * y >= x);
 }
 
 // Key steps of a piece, where num_splits leaves the choice (all blocks compute
@@ -151,20 +165,20 @@ __device__ __forceinline__ Shapes gather_shapes(const PagedArgs &a, Shape *at, i
 template <typename F>
 __device__ __forceinline__ int choose_piece(const PagedArgs &a, float work, float pairs,
                                             int longest, const F &pieces) {
+  const float wave = (float)a.wave;
   // least piece that makes about n full ones
   const auto least = [&](float n) {
-    return max(kMinPieceSteps, (int)fminf(work / n * 1.0001f, 1e9f) + 1);
+    return max(kMinPieceSteps, (int)fminf(__fdividef(work, n) * 1.0001f, 1e9f) + 1);
   };
   // Pieces make waves of blocks, and a wave that is started for a few of them
-  // is lost.  Pairs of a tile and a head end in a part of a piece, half of one on
-  // average: n full pieces make n + pairs / 2.  Take the number of waves whose
-  // time -- a piece's steps, and kBlockSteps for a block's start and end -- is
-  // least.  (24 sequences of 2-9 tokens, d = 64: 2.3 waves 127 us, just below two
-  // 109.)
-  int ps = least(2.f * (float)a.wave);  // more pairs than max_waves hold
+  // is lost.  Pairs of a tile and a head end in a part of a piece, half of one on average: n full
+  // pieces make n + pairs / 2.  Take the number of waves whose time -- a piece's
+  // steps, and kBlockSteps for a block's start and end -- is least.  (24 sequences
+  // of 2-9 tokens, d = 64: 2.3 waves 127 us, just below two 109.)
+  int ps = least(2.f * wave);  // more pairs than max_waves hold
   float best = INFINITY, room = 0.f;
   for (int k = 1; k <= a.max_waves; ++k) {
-    const float blocks = (float)k * (float)a.wave;
+    const float blocks = (float)k * wave;
     if (pairs >= 0.9f * blocks) continue;
     const int p = least(0.98f * blocks - 0.5f * pairs);
     const float time = (float)k * (float)(p + kBlockSteps);
@@ -175,14 +189,13 @@ __device__ __forceinline__ int choose_piece(const PagedArgs &a, float work, floa
     }
   }
   // Whole pairs, unless pieces and the joining of them are worth it.
-  if (ceilf(pairs / (float)a.wave) * (float)(longest + kBlockSteps) <= best + kJoinSteps)
+  if (ceilf(__fdividef(pairs, wave)) * (float)(longest + kBlockSteps) <= best + kJoinSteps)
     return INT32_MAX;
   // The average may be off, and the grid has to hold every item.  Where
   // max_waves is 3 it holds all pairs and two waves of full pieces besides; else
   // the size that fits in any case replaces one that misses the wave.
   if (room > 0.f && pieces(ps) > room)
-    ps = a.max_waves == 3 && pairs >= 0.7f * room ? max(ps, least(2.f * (float)a.wave))
-                                                  : least(room - pairs);
+    ps = a.max_waves == 3 && pairs >= 0.7f * room ? max(ps, least(2.f * wave)) : least(room - pairs);
   return ps;
 }
 
@@ -197,46 +210,53 @@ __device__ __forceinline__ bool find_item(const PagedArgs &a, const Shapes &sh, 
     if (i >= a.batch) return Shape{0, 0};
     return i < kMaxShapes ? sh.at[i] : shape_of(a, paged_seq(a, i), pos, bn);
   };
+  const Shape first = shape(lane);
   int piece_steps = INT32_MAX;
+  float inv_steps = 0.f;
   if (a.num_splits == 0) {
     piece_steps = choose_piece(a, sh.work * (float)nh, sh.pairs * (float)nh, sh.longest, [&](int ps) {
-      float n = 0.f;
-      for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      const float inv = __frcp_rn((float)ps);
+      float n = (float)first.tiles * (float)div_up(first.steps, ps, inv);
+      for (int b0 = 32; b0 < a.batch; b0 += 32) {
         const Shape x = shape(b0 + lane);
-        n += (float)x.tiles * (float)((x.steps + ps - 1) / ps);
+        n += (float)x.tiles * (float)div_up(x.steps, ps, inv);
       }
       return warp_sum(n) * (float)nh;
     });
+    inv_steps = __frcp_rn((float)piece_steps);
   }
   const auto pieces_of = [&](const Shape &x) {
     if (a.num_splits > 0) return max(1, min(a.num_splits, x.steps));
-    return x.steps <= piece_steps ? 1 : (x.steps + piece_steps - 1) / piece_steps;
+    return x.steps <= piece_steps ? 1 : div_up(x.steps, piece_steps, inv_steps);
   };
   const auto times = [&](const Shape &x, int p) {
-    return (uint32_t)min((uint64_t)x.tiles * nh * p, (uint64_t)INT32_MAX);
+    return (float)x.tiles * (float)(nh * p) > 2e9f ? (uint32_t)INT32_MAX
+                                                   : (uint32_t)(x.tiles * nh * p);
   };
   // Order: sequences of several tiles are bound by the tensor cores, those of
   // one tile mostly by memory.  Where a call has both, their items alternate in
   // proportion, so that the two kinds of blocks run beside one another.
   // (47 single tokens and a chunk of 2001: 285 us in sequence order, 266 so.)
-  uint32_t n_long = 0, n_all = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    const Shape x = shape(b0 + lane);
-    const uint32_t n = min(times(x, pieces_of(x)), 1u << 24);
-    n_all = add_sat(n_all, __reduce_add_sync(0xffffffffu, n));
-    n_long = add_sat(n_long, __reduce_add_sync(0xffffffffu, x.tiles > 1 ? n : 0));
-  }
-  const bool mixed = n_long > 0 && n_long < n_all && n_all < (1u << 16);
-  bool is_long = false;
+  bool mixed = sh.long_pairs > 0.f && sh.long_pairs < sh.pairs, is_long = false;
   if (mixed) {
-    if (idx >= n_all) return false;
-    const uint32_t before = idx * n_long / n_all;  // long items before this one
-    is_long = (idx + 1) * n_long / n_all > before;
-    idx = is_long ? before : idx - before;
+    uint32_t n_long = 0, n_all = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      const Shape x = b0 == 0 ? first : shape(b0 + lane);
+      const uint32_t n = min(times(x, pieces_of(x)), 1u << 24);
+      n_all = add_sat(n_all, __reduce_add_sync(0xffffffffu, n));
+      n_long = add_sat(n_long, __reduce_add_sync(0xffffffffu, x.tiles > 1 ? n : 0));
+    }
+    mixed = n_all < (1u << 16);  // (the products below)
+    if (mixed) {
+      if (idx >= n_all) return false;
+      const uint32_t before = idx * n_long / n_all;  // long items before this one
+      is_long = (idx + 1) * n_long / n_all > before;
+      idx = is_long ? before : idx - before;
+    }
   }
   uint32_t base = 0, slots = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    const Shape x = shape(b0 + lane);
+    const Shape x = b0 == 0 ? first : shape(b0 + lane);
     const int pieces = pieces_of(x);
     const uint32_t all = times(x, pieces), n = mixed && is_long != (x.tiles > 1) ? 0 : all;
     uint32_t incl = n;
@@ -249,21 +269,22 @@ __device__ __forceinline__ bool find_item(const PagedArgs &a, const Shapes &sh, 
     const uint32_t cut = pieces > 1 ? all : 0;  // slots
     if (hit) {
       const int src = __ffs(hit) - 1;
-      slots = add_sat(slots, __reduce_add_sync(0xffffffffu, lane < src ? cut : 0));
-      const uint32_t local = idx - base - __shfl_sync(0xffffffffu, incl - n, src);
       it.seq = b0 + src;
       it.s = paged_seq(a, it.seq);
+      slots = add_sat(slots, __reduce_add_sync(0xffffffffu, lane < src ? cut : 0));
+      const uint32_t local = idx - base - __shfl_sync(0xffffffffu, incl - n, src);
       it.pieces = __shfl_sync(0xffffffffu, pieces, src);
       const int tiles = __shfl_sync(0xffffffffu, x.tiles, src);
       // heads fastest (they share a sequence's pages and, in L2, its K and V),
       // then pieces; the last positions, which see the most keys, first
       const uint32_t upper = local / (uint32_t)nh;
       it.head = (int)(local - upper * nh);
-      const uint32_t m = upper / (uint32_t)it.pieces;
+      const uint32_t m = it.pieces == 1 ? upper : upper / (uint32_t)it.pieces;
       it.piece = (int)(upper - m * it.pieces);
       it.m0 = (tiles - 1 - (int)m) * pos;
       // pieces of one tile and head are nh slots apart
       it.slot = it.pieces > 1 ? (int)add_sat(slots, local) : -1;
+      it.stride = nh;
       return it.m0 >= 0;
     }
     base = add_sat(base, __shfl_sync(0xffffffffu, incl, 31));
@@ -347,80 +368,99 @@ __device__ __forceinline__ bool wait_warp(Shared &sh, uint64_t *bar, uint32_t pa
 template <typename T> struct IsBf16 { static constexpr int v = 0; };
 template <> struct IsBf16<__nv_bfloat16> { static constexpr int v = 1; };
 
-// Joins the n pieces of a pair, by 128 NT threads: with l_p the log2-sums, L =
-// log2 sum 2^l_p and O = sum 2^(l_p - L) O_p, in key order, so the result does
-// not depend on who finishes last.  The weights 2^(l_p - L) of as many rows as
-// fit go to shared memory first; then a thread takes four columns of a row.
-// (Read past L1: other blocks have written the pieces.)
-template <typename T, int D, int NT>
-__device__ __forceinline__ void join_pieces(const PagedArgs &a, const Item &it, int n, int nh,
-                                            int slot0, int tile_pos, int tid, float *w, int w_floats) {
-  constexpr int kQuads = D / 4, kThreads = 128 * NT;
-  const int pg = a.pack, lane = tid & 31;
-  const int positions = min(it.s.lq - it.m0, NT * tile_pos);
-  const int rows = positions * pg, tile_rows = tile_pos * pg;
-  const int64_t step = (int64_t)nh * (NT * kBM);  // rows from a piece to the next
-  // row x of the pair in its slot, and in the output
-  const auto part_row = [&](int x) {
-    const int t = NT == 2 && x >= tile_rows ? 1 : 0;
-    return (int64_t)slot0 * (NT * kBM) + t * kBM + (x - t * tile_rows);
-  };
-  const auto out_row = [&](int x, int &hr) {
-    const int p = x / pg;
-    hr = pg > 1 ? it.head * pg + x - p * pg : it.head;
-    return (int64_t)(it.s.q0 + it.m0 + p);
-  };
-  const int batch = max(1, min(rows, w_floats / n));
-  for (int x0 = 0; x0 < rows; x0 += batch) {
-    const int x1 = min(rows, x0 + batch);
-    // one warp per row, lanes over the pieces; few pieces: several rows a warp
-    int lanes = 32;
-    while (lanes > 1 && lanes / 2 >= n) lanes /= 2;
-    const int sub = lane & (lanes - 1);
-    for (int xb = x0 + (tid - sub) / lanes; xb - (lane - sub) / lanes < x1; xb += kThreads / lanes) {
-      const bool on = xb < x1;
-      const float *l = a.lse_part + (on ? part_row(xb) : 0);
-      float m = -INFINITY, sum = 0.f;
-      if (on)
-        for (int p = sub; p < n; p += lanes) m = fmaxf(m, __ldcg(l + p * step));
-      for (int o = lanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (on)
-        for (int p = sub; p < n; p += lanes) {
-          const float e = m > -INFINITY ? exp2f(__ldcg(l + p * step) - m) : 0.f;
-          w[(xb - x0) * n + p] = e;
-          sum += e;
+// Joins the n pieces of a pair: with l_p the log2-sums, L = log2 sum 2^l_p and
+// O = sum 2^(l_p - L) O_p, in key order, so the result does not depend on who
+// finishes last.  Called by the kWarps softmax warps, once per block at most and
+// with few instructions between them, so what counts is the number of trips to
+// L2 one after another: a warp takes kR rows at a time, a lane four columns (and
+// for d = 256 four more), asks for the sums and the first kP pieces at once, and
+// has the weights ready in its lanes when the pieces arrive.  (Read past L1:
+// other blocks have written them.)
+template <typename T, int D, int NT, int kWarps, int kR, int kP>
+__device__ __forceinline__ void join_rows(const PagedArgs &a, const Item &it, int n, int slot0,
+                                          int tile_pos, int warp) {
+  constexpr int LPR = D / 4 < 32 ? D / 4 : 32;  // lanes of a row
+  constexpr int QP = D / 4 / LPR;               // column quads of a lane
+  constexpr int RPW = 32 / LPR;                 // rows side by side in a warp
+  const int lane = threadIdx.x & 31, sub = lane % LPR, pg = a.pack;
+  const int rows = min(it.s.lq - it.m0, NT * tile_pos) * pg, tile_rows = tile_pos * pg;
+  const uint32_t inv_pg = (65536 + pg - 1) / pg;  // x / pg = x inv_pg >> 16 for x < 256
+  const int64_t step = (int64_t)it.stride * (NT * kBM);  // rows from a piece to the next
+  const float *l_at = a.lse_part + (int64_t)slot0 * (NT * kBM);
+  const float4 *o_at = reinterpret_cast<const float4 *>(a.o_part) +
+                       (int64_t)slot0 * (NT * kBM) * (D / 4) + sub;
+  constexpr int kStep = kWarps * RPW;  // rows from one of a warp's to its next
+  for (int x0 = warp * RPW; x0 < rows; x0 += kR * kStep) {
+    const int xl = x0 + lane / LPR;
+    int64_t at[kR];  // of the row in its slot
+    float l[kR], w[kR], lse[kR];
+    float4 v[kR][QP][kP];
+#pragma unroll
+    for (int k = 0; k < kR; ++k) {
+      const int x = min(xl + k * kStep, rows - 1);
+      at[k] = x + (NT == 2 && x >= tile_rows ? kBM - tile_rows : 0);
+      l[k] = sub < n ? __ldcg(l_at + at[k] + sub * step) : -INFINITY;
+    }
+    const auto load = [&](int p0) {
+#pragma unroll
+      for (int k = 0; k < kR; ++k)
+#pragma unroll
+        for (int p = 0; p < kP; ++p)
+#pragma unroll
+          for (int q = 0; q < QP; ++q)
+            if (p0 + p < n) v[k][q][p] = __ldcg(o_at + (at[k] + (p0 + p) * step) * (D / 4) + q * LPR);
+    };
+    load(0);
+#pragma unroll
+    for (int k = 0; k < kR; ++k) {
+      float m = l[k], sum = 0.f;
+      for (int p = sub + LPR; p < n; p += LPR) m = fmaxf(m, __ldcg(l_at + at[k] + p * step));
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float ref = m > -INFINITY ? m : 0.f;
+      w[k] = exp2f(l[k] - ref);
+      sum = w[k];
+      for (int p = sub + LPR; p < n; p += LPR) sum += exp2f(__ldcg(l_at + at[k] + p * step) - ref);
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      lse[k] = sum > 0.f ? (ref + log2f(sum)) * kLn2 : -INFINITY;
+      l[k] = sum > 0.f ? ref + log2f(sum) : INFINITY;  // weights 2^(l_p - this)
+      w[k] = sum > 0.f ? w[k] / sum : 0.f;
+    }
+    float o[kR][QP][4] = {};
+    for (int p0 = 0; p0 < n; p0 += kP) {
+      if (p0 > 0) load(p0);
+#pragma unroll
+      for (int k = 0; k < kR; ++k)
+#pragma unroll
+        for (int p = 0; p < kP; ++p) {
+          if (p0 + p >= n) break;
+          // (beyond the lanes' own pieces: looked up again)
+          const float wp = p0 + p < LPR
+                               ? __shfl_sync(0xffffffffu, w[k], p0 + p, LPR)
+                               : exp2f(__ldcg(l_at + at[k] + (p0 + p) * step) - l[k]);
+#pragma unroll
+          for (int q = 0; q < QP; ++q) {
+            o[k][q][0] = fmaf(wp, v[k][q][p].x, o[k][q][0]);
+            o[k][q][1] = fmaf(wp, v[k][q][p].y, o[k][q][1]);
+            o[k][q][2] = fmaf(wp, v[k][q][p].z, o[k][q][2]);
+            o[k][q][3] = fmaf(wp, v[k][q][p].w, o[k][q][3]);
+          }
         }
-      for (int o = lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
-      if (on) {
-        for (int p = sub; p < n; p += lanes) w[(xb - x0) * n + p] *= inv;
-        if (sub == 0) {
-          int hr;
-          const int64_t row = out_row(xb, hr);
-          a.lse[(int64_t)hr * a.total_q + row] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
-        }
+    }
+#pragma unroll
+    for (int k = 0; k < kR; ++k) {
+      const int x = xl + k * kStep;
+      if (x < rows) {
+        const int p = (int)(x * inv_pg >> 16);
+        const int hr = pg > 1 ? it.head * pg + x - p * pg : it.head;
+        const int64_t row = it.s.q0 + it.m0 + p;
+        T *dst = static_cast<T *>(a.o) + (row * a.hq + hr) * D + sub * 4;
+#pragma unroll
+        for (int q = 0; q < QP; ++q) store_vec<T, 4>(dst + q * LPR * 4, o[k][q]);
+        if (sub == 0) a.lse[(int64_t)hr * a.total_q + row] = lse[k];
       }
     }
-    named_bar_sync(1, kThreads);
-#pragma unroll 2
-    for (int y = tid; y < (x1 - x0) * kQuads; y += kThreads) {
-      const int x = y / kQuads, c = y % kQuads;
-      const float4 *src = reinterpret_cast<const float4 *>(a.o_part + part_row(x0 + x) * D) + c;
-      float o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-      for (int p = 0; p < n; ++p) {
-        const float wp = w[x * n + p];
-        const float4 v = __ldcg(src + p * step * kQuads);
-        o[0] = fmaf(wp, v.x, o[0]);
-        o[1] = fmaf(wp, v.y, o[1]);
-        o[2] = fmaf(wp, v.z, o[2]);
-        o[3] = fmaf(wp, v.w, o[3]);
-      }
-      int hr;
-      const int64_t row = out_row(x0 + x, hr);
-      store_vec<T, 4>(static_cast<T *>(a.o) + (row * a.hq + hr) * D + c * 4, o);
-    }
-    named_bar_sync(1, kThreads);
   }
 }
 
@@ -444,7 +484,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pg = a.pack;
   // shapes of the sequences: every warp but the one that allocates TMEM
-  Shapes shapes{reinterpret_cast<Shape *>(smem), 0.f, 0.f, 0};
+  Shapes shapes{reinterpret_cast<Shape *>(smem), 0.f, 0.f, 0.f, 0};
   constexpr int kGather = C::kThreads / 32 - 1;
   if (warp == 1) {
     tmem_alloc(&sh.tmem_base, C::kTmemCols);
@@ -484,13 +524,13 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
     for (int w = 0; w < kGather && w * 32 < a.batch; ++w) {
       shapes.work += sh.sums[w].work;
       shapes.pairs += sh.sums[w].pairs;
+      shapes.long_pairs += sh.sums[w].long_pairs;
       shapes.longest = max(shapes.longest, sh.sums[w].longest);
     }
     Item it{};
     it.pieces = 1;
     const bool found = find_item(a, shapes, blockIdx.x, tile_pos * NT, BN, it);
     const Piece p = piece_of(a, it, tile_pos * NT, BN, found);
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // paged_zero_kernel
     early = fetch_boxes(a, it, p, BN / box_rows, box_rows, p.n_lo * BN, 0);
     if (lane == 0) {
       sh.item = it;
@@ -934,18 +974,23 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
     if (kCut && live && reinterpret_cast<volatile int &>(sh.item.pieces) > 1) {
       named_bar_sync(1, 128 * NT);
       const Item jt = sh.item;
-      const int nh = a.pack > 1 ? a.hkv : a.hq, n = sh.piece.written;
-      const int slot0 = jt.slot - jt.piece * nh;  // of the first piece
+      const int n = sh.piece.written;
+      const int slot0 = jt.slot - jt.piece * jt.stride;  // of the first piece
       const int tid = threadIdx.x - 32 * C::kSoftmaxWarp0;
-      const bool fits = slot0 + (n - 1) * nh < a.slots;
+      const bool fits = slot0 + (n - 1) * jt.stride < a.slots;
       if (tid == 0) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // paged_zero_kernel, long done
         sh.joins = fits && atomicAdd(&a.written[slot0], 1) == n - 1;
         __threadfence();
       }
       named_bar_sync(1, 128 * NT);
-      if (sh.joins)
-        join_pieces<T, D, NT>(a, jt, n, nh, slot0, tile_pos, tid, reinterpret_cast<float *>(smem),
-                              C::kSmemData / 4);
+      if (sh.joins) {
+        // few rows (single tokens): many pieces at a time; else many rows
+        if (min(jt.s.lq - jt.m0, NT * tile_pos) * a.pack <= 4 * C::kSoftmaxWarps)
+          join_rows<T, D, NT, C::kSoftmaxWarps, 1, 4>(a, jt, n, slot0, tile_pos, tid >> 5);
+        else
+          join_rows<T, D, NT, C::kSoftmaxWarps, 2, 4>(a, jt, n, slot0, tile_pos, tid >> 5);
+      }
     }
   }
   tc_fence_before();
