@@ -595,14 +595,16 @@ attn_status attn_fwd_paged(const void *q, const void *k_cache, const void *v_cac
   return launched(launch_paged_tc(a, plan, stream));
 }
 
-uint64_t attn_rope_phase(double inv_freq) {
-  // the fraction of a turn per position, scaled by 2^64 in two exact steps
-  // (a fraction that rounds up to a whole turn is phase 0)
-  const double turns = inv_freq / 6.283185307179586476925;
-  const double frac = turns - floor(turns);
-  const double hi = floor(ldexp(frac, 32));
-  const double lo = rint(ldexp(ldexp(frac, 32) - hi, 32));
-  return ((uint64_t)hi << 32) + (uint64_t)lo;
+uint64_t attn_rope_phase(double inv_freq) { return rope_phase(inv_freq); }
+
+attn_status attn_rope_phases(const double *inv_freq, uint64_t *phases, int n,
+                             attn_stream_t stream) {
+  if (n < 0) return ATTN_ERR_INVALID;
+  if (n == 0) return ATTN_OK;
+  if (!inv_freq || !phases || (reinterpret_cast<uintptr_t>(inv_freq) & 7) ||
+      (reinterpret_cast<uintptr_t>(phases) & 7))
+    return ATTN_ERR_INVALID;
+  return launched(launch_rope_phases(inv_freq, phases, n, stream));
 }
 
 attn_status attn_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out,

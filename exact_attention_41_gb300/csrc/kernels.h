@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cudaTypedefs.h>
+#include <math.h>
 
 #include <atomic>
 
@@ -112,6 +113,16 @@ struct PagedPlan {
 PagedPlan paged_plan(int batch, int total_q, int hq, int hkv, int d, int num_splits, int64_t keys,
                      int sms);
 
+// The fraction of a turn per position of a frequency in radians, times 2^64,
+// in two exact steps (a fraction that rounds up to a whole turn is phase 0).
+__host__ __device__ inline uint64_t rope_phase(double inv_freq) {
+  const double turns = inv_freq / 6.283185307179586476925;
+  const double high = (turns - floor(turns)) * 4294967296.0;
+  if (!(high >= 0.0 && high <= 4294967296.0)) return 0;  // not finite
+  const double whole = floor(high);
+  return ((uint64_t)whole << 32) + (uint64_t)rint((high - whole) * 4294967296.0);
+}
+
 // Per-head norm and rotation (attn_qk_norm_rope, its backward, and
 // attn_kvcache_append).  *_rs: elements between consecutive token rows; for
 // the append k_out_rs and v_out_rs are the page strides of the caches.
@@ -213,6 +224,8 @@ cudaError_t launch_paged_tc(const PagedArgs &a, const PagedPlan &plan, cudaStrea
 // Forward of the norm and rotation, or the append when a.cu_seqlens is set.
 cudaError_t launch_norm_rope(const RopeArgs &a, int sms, cudaStream_t st);
 cudaError_t launch_norm_rope_bwd(const RopeArgs &a, int sms, cudaStream_t st);
+// phases[j] = rope_phase(inv_freq[j]) for j < n.
+cudaError_t launch_rope_phases(const double *inv_freq, uint64_t *phases, int n, cudaStream_t st);
 // Most blocks of the backward, each of which writes d floats of workspace.
 int rope_bwd_blocks(int sms);
 // cache_seqlens[i] += s_new for i < b.

@@ -412,6 +412,11 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const RopeArgs a, int
   }
 }
 
+__global__ void rope_phases_kernel(const double *inv_freq, uint64_t *phases, int n) {
+  const int j = blockIdx.x * blockDim.x + threadIdx.x;
+  if (j < n) phases[j] = rope_phase(inv_freq[j]);
+}
+
 template <typename T, int D>
 cudaError_t fwd(RopeArgs a, int sms, cudaStream_t st) {
   constexpr int HPW = 32 / (D / 16);
@@ -475,6 +480,12 @@ cudaError_t bwd(const RopeArgs &a, int sms, cudaStream_t st) {
 
 // (at least one block each for queries and keys)
 int rope_bwd_blocks(int sms) { return std::max(2, kBwdBlocks * sms); }
+
+cudaError_t launch_rope_phases(const double *inv_freq, uint64_t *phases, int n, cudaStream_t st) {
+  rope_phases_kernel<<<(n + 127) / 128, 128, 0, st>>>(inv_freq, phases, n);
+  count_launches(1);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_norm_rope(const RopeArgs &a, int sms, cudaStream_t st) {
   const bool bf = a.dtype == ATTN_BF16;

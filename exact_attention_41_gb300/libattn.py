@@ -51,6 +51,7 @@ _SIGS = {
     "attn_fwd_paged": ([_vp] * 5 + [_i64] * 3 + [_vp] * 3 + [_i] * 10 +
                        [_f, _i, _i, _i, _f, _i, _vp, _sz, _vp], _i),
     "attn_rope_phase": ([ctypes.c_double], ctypes.c_uint64),
+    "attn_rope_phases": ([_vp, _vp, _i, _vp], _i),
     "attn_qk_norm_rope": ([_vp] * 4 + [_i64] * 4 + [_vp, _vp, _f, _vp, _i, _i, _vp] + [_i] * 6 +
                           [_vp], _i),
     "attn_qk_norm_rope_bwd_workspace_size": ([_i] * 5, _sz),
@@ -565,17 +566,15 @@ def fwd_paged(q, k_cache, v_cache, cu_seqlens_q, cache_seqlens, *, block_table=N
 
 def rope_phases(inv_freq, device=None):
     """The phases of the rotation from its frequencies in radians per position
-    (a sequence or tensor of rot/2 numbers, read in 64 bits), as an int64
+    (a sequence or tensor of rot/2 numbers, read in 64 bits; finite), as an int64
     tensor on `device` (default: that of inv_freq, or the current CUDA device)."""
     torch = _torch()
-    f = torch.as_tensor(inv_freq, dtype=torch.float64)
-    if device is None:
-        device = f.device if f.is_cuda else torch.device("cuda", torch.cuda.current_device())
-    values = f.flatten().tolist()
-    _need(all(math.isfinite(x) for x in values), "frequencies must be finite")
-    bits = [lib().attn_rope_phase(x) for x in values]
-    return torch.tensor([b - (1 << 64) if b >= 1 << 63 else b for b in bits], dtype=torch.int64,
-                        device=device)
+    if device is None and not getattr(inv_freq, "is_cuda", False):
+        device = "cuda"
+    f = torch.as_tensor(inv_freq, dtype=torch.float64, device=device).flatten().contiguous()
+    phases = torch.empty(f.shape, dtype=torch.int64, device=f.device)
+    _call(lib().attn_rope_phases, (f.data_ptr(), phases.data_ptr(), f.numel()), (f, phases))
+    return phases
 
 
 def _rope_args(phases, q_weight, k_weight, ref):

@@ -315,8 +315,14 @@ attn_status attn_fwd_paged(const void *q, const void *k_cache, const void *v_cac
  * and >= 0.  Arithmetic is fp32, rounded once to dtype.
  */
 
-/* The phase of a frequency in radians per position (finite).  Host only. */
+/* The phase of a frequency in radians per position (0 for one that is not
+ * finite).  Host only. */
 uint64_t attn_rope_phase(double inv_freq);
+
+/* The same on the device: phases[j] = attn_rope_phase(inv_freq[j]) for j < n,
+ * both DEVICE arrays, 8-byte aligned.  n == 0 is a no-op. */
+attn_status attn_rope_phases(const double *inv_freq, uint64_t *phases, int n,
+                             attn_stream_t stream);
 
 /*
  * Norm and rotation of q (b,s,hq,d) and k (b,s,hkv,d) into q_out and k_out of

@@ -101,6 +101,20 @@ def test_forward(case):
                 np.testing.assert_array_equal(host(got).reshape(want.shape)[..., rot:], x[..., rot:])
 
 
+def test_phases_on_the_device_are_those_of_the_host():
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    rng = np.random.default_rng(3)
+    f = np.concatenate([freqs(256), rng.standard_normal(300) * 10.0 ** rng.integers(-12, 8, 300),
+                        [0.0, 2 * np.pi, -1e-300, 5e-324, np.inf, -np.inf, np.nan, 1e300]])
+    want = np.array([libattn.lib().attn_rope_phase(float(x)) for x in f], np.uint64)
+    for given in (f, torch.tensor(f), torch.tensor(f, device="cuda"), list(f)):
+        got = libattn.rope_phases(given).cpu().numpy().view(np.uint64)
+        np.testing.assert_array_equal(got, want)
+
+
 def test_far_positions_keep_their_angles():
     """Positions up to 2^31 - 1, and negative ones: the angle is exact modulo a turn."""
     import torch

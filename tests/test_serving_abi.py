@@ -123,6 +123,15 @@ def test_phases(lib):
     assert abs(got - frac) < 1e-6   # the 64-bit frequency itself: 2^-53 * 0.05 * 1e9 = 6e-9 turns
 
 
+def test_phases_of_what_is_no_frequency(lib):
+    for f in (float("inf"), float("-inf"), float("nan")):
+        assert lib.attn_rope_phase(f) == 0
+    assert lib.attn_rope_phases(FAKE, FAKE, -1, None) == 1
+    assert lib.attn_rope_phases(None, FAKE, 4, None) == 1
+    assert lib.attn_rope_phases(FAKE, ctypes.c_void_p(0x10004), 4, None) == 1
+    assert lib.attn_rope_phases(None, None, 0, None) == 0
+
+
 def test_binding_refusals():
     torch = pytest.importorskip("torch")
     q = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
