@@ -57,6 +57,7 @@ const DeviceInfo *device_info() {
 
 constexpr size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // Checks shared by every entry point.  win_r is normalised (causal -> 0).
@@ -543,6 +544,12 @@ attn_status attn_fwd_paged(const void *q, const void *k_cache, const void *v_cac
     return ATTN_ERR_INVALID;
   for (const void *p : {q, k_cache, v_cache, (const void *)out, (const void *)workspace})
     if (!aligned16(p)) return ATTN_ERR_INVALID;
+  if (!aligned4(lse) || !aligned4(cu_seqlens_q) || !aligned4(cache_seqlens) ||
+      !aligned4(block_table))
+    return ATTN_ERR_INVALID;
+  // wider than any sequence is unbounded (and would not add to a position)
+  if (win_l > INT32_MAX / 2) win_l = -1;
+  if (win_r > INT32_MAX / 2) win_r = -1;
   if ((int64_t)total_q * hq > INT32_MAX || hq > 65535) return ATTN_ERR_UNSUPPORTED;
   const DeviceInfo *di = device_info();
   const PagedPlan plan =
@@ -624,6 +631,7 @@ attn_status attn_qk_norm_rope(const void *q, const void *k, void *q_out, void *k
   if ((hq > 0 && (!q || !q_out)) || (hkv > 0 && (!k || !k_out))) return ATTN_ERR_INVALID;
   for (const void *p : {q, k, (const void *)q_out, (const void *)k_out})
     if (!aligned16(p)) return ATTN_ERR_INVALID;
+  if (!aligned4(positions)) return ATTN_ERR_INVALID;
   if ((int64_t)b * s > INT32_MAX / 64) return ATTN_ERR_UNSUPPORTED;
   RopeArgs a{};
   a.q = q;
@@ -688,6 +696,7 @@ attn_status attn_qk_norm_rope_bwd(const void *q, const void *k, const void *dq_o
   for (const void *p : {q, k, dq_out, dk_out, (const void *)dq, (const void *)dk,
                         (const void *)dq_weight, (const void *)dk_weight, (const void *)workspace})
     if (!aligned16(p)) return ATTN_ERR_INVALID;
+  if (!aligned4(positions)) return ATTN_ERR_INVALID;
   if ((int64_t)b * s > INT32_MAX / 64) return ATTN_ERR_UNSUPPORTED;
   const size_t need = attn_qk_norm_rope_bwd_workspace_size(b, s, hq, hkv, d);
   if (need > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
@@ -756,6 +765,8 @@ attn_status attn_kvcache_append(const void *q, void *q_out, const void *k_new, c
   for (const void *p : {q, (const void *)q_out, k_new, v_new, (const void *)k_cache,
                         (const void *)v_cache})
     if (!aligned16(p)) return ATTN_ERR_INVALID;
+  if (!aligned4(cu_seqlens) || !aligned4(cache_seqlens) || !aligned4(block_table))
+    return ATTN_ERR_INVALID;
   if (total > INT32_MAX / 64) return ATTN_ERR_UNSUPPORTED;
   RopeArgs a{};
   a.q = q;

@@ -146,6 +146,13 @@ def test_keys_of_another_origin_and_empty_rows(splits):
     assert (host(o)[40:47] == 0).all() and np.isneginf(host(lse)[:, 40:47]).all()
 
 
+def test_windows_wider_than_any_sequence():
+    c = make(14, [40, 1, 7], [100, 300, 0], 4, 2, 64, 16, syn.F16)
+    big = 2 ** 31 - 1
+    run(c, window=(big, big))
+    run(c, causal=True, window=(big, 0))
+
+
 def test_many_sequences():
     """More sequences than a warp has lanes, most of one token, some empty."""
     rng = np.random.default_rng(5)

@@ -10,6 +10,7 @@ from exact_attention_41_gb300 import libattn
 
 FAKE = ctypes.c_void_p(0x10000)  # never dereferenced: validation fails first
 ODD = ctypes.c_void_p(0x10008)
+BYTE = ctypes.c_void_p(0x10002)
 BIG = 1 << 40
 
 
@@ -32,6 +33,7 @@ def paged(lib, **over):
     (dict(page=0), 1), (dict(page=-16), 1), (dict(max_pages=0), 1), (dict(num_pages=-1), 1),
     (dict(splits=-1), 1), (dict(q=None), 1), (dict(k=None), 1), (dict(out=None), 1),
     (dict(lse=None), 1), (dict(cu=None), 1), (dict(cs=None), 1), (dict(q=ODD), 1), (dict(v=ODD), 1),
+    (dict(lse=BYTE), 1), (dict(cu=BYTE), 1), (dict(cs=BYTE), 1), (dict(bt=BYTE), 1),
     (dict(q_rs=4 * 128 - 8), 1), (dict(q_rs=4 * 128 + 4), 1), (dict(k_ps=64 * 2 * 128 - 8), 1),
     (dict(v_ps=64 * 2 * 128 + 4), 1), (dict(bt=None), 1), (dict(bt=None, num_pages=2), 1),
     (dict(scale=float("nan")), 1), (dict(wl=-2), 1), (dict(cap=float("nan")), 1),
@@ -60,7 +62,7 @@ def rope(lib, **over):
 
 @pytest.mark.parametrize("over,status", [
     (dict(d=80), 2), (dict(dtype=-1), 1), (dict(rot=8), 1), (dict(rot=144), 1), (dict(rot=-16), 1),
-    (dict(ph=None), 1), (dict(ph=ODD), 1), (dict(wq=ODD), 1), (dict(eps=-1.0), 1),
+    (dict(ph=None), 1), (dict(ph=ODD), 1), (dict(pos=BYTE), 1), (dict(wq=ODD), 1), (dict(eps=-1.0), 1),
     (dict(eps=float("inf")), 1), (dict(q=None), 1), (dict(ko=None), 1), (dict(qo=ODD), 1),
     (dict(s0=4 * 128 - 8), 1), (dict(s2=4 * 128 + 1), 1), (dict(b=-1), 1), (dict(hq=-1), 1),
     (dict(s2=4 * 128 + 8), 1),                       # in place (q_out is q), other row places
@@ -80,7 +82,7 @@ def test_norm_rope_backward_refusals(lib):
 
     assert call(dwq=None) == 1 and call(dk=None) == 1 and call(q=None) == 1
     assert call(n=16) == 3 and call(ws=None) == 3
-    assert call(ws=ODD) == 1 and call(rot=72) == 1 and call(d=32) == 2
+    assert call(ws=ODD) == 1 and call(rot=72) == 1 and call(d=32) == 2 and call(pos=BYTE) == 1
     assert call(s2=4 * 64 + 8) == 1                  # dq is dq_out, but in other row places
     assert call(hq=0, hkv=0) == 0
     assert lib.attn_qk_norm_rope_bwd_workspace_size(0, 8, 4, 2, 64) == 0
@@ -97,7 +99,7 @@ def test_append_refusals(lib):
     for over in (dict(k=None), dict(v=None), dict(qo=None), dict(kc=None), dict(cu=None),
                  dict(cs=None), dict(page=0), dict(kp=5 * 2 * 64 - 8), dict(vp=5 * 2 * 64 + 4),
                  dict(hkv=0), dict(rot=24), dict(s1=8), dict(bt=None), dict(vc=ODD),
-                 dict(total=-1), dict(batch=-1)):
+                 dict(cu=BYTE), dict(cs=BYTE), dict(bt=BYTE), dict(total=-1), dict(batch=-1)):
         assert call(**over) == 1, over
     assert call(total=0) == 0 and call(batch=0) == 0
 
