@@ -95,14 +95,13 @@ struct PagedArgs {
   // of cut rows write partial results to one of `slots` slots of the workspace.
   int pack;                     // query heads that share a tile: g or 1
   int num_splits, wave, max_waves, slots;
-  float *o_part;                // (slots, rows of a block, d)
-  float *lse_part;              // (slots, rows of a block), log2 units
+  float *o_part;                // (slots, 128, d)
+  float *lse_part;              // (slots, 128), log2 units
   int *written;                 // (slots) pieces written, at a pair's first slot
 };
 
 // How attn_fwd_paged cuts its work; host only, from the sizes of the call.
 struct PagedPlan {
-  int layout;                   // query tiles of 128 rows per block
   int pack;
   int tile_pos;                 // query positions of one 128-row tile
   int num_splits, wave, max_waves;

@@ -47,33 +47,42 @@ using namespace sm103;
 constexpr int kBM = 128;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O when max grows > 256x
 constexpr int kMaxStages = 5;
-constexpr int kMaxWarps = 12;
+constexpr int kMaxWarps = 7;
+constexpr int kJoinRing = 8;        // tiles of 8 KB
+constexpr int kJoinWeights = 8192;  // rows x pieces
 constexpr int kMinPieceSteps = 4;          // shortest piece worth a block and a partial result
 constexpr int kBlockSteps = 8;             // a block's start and end, in steps
-constexpr int kJoinSteps = 4;              // what joining pieces adds to a call, in steps
+// what joining adds to a call, in steps: a step per so many values of a piece,
+// and once (rows on their way to the workspace and back) per so many of a tile
+constexpr float kJoinRate = 5000.f, kJoinBase = 1400.f;
 
-// NT query tiles per block, BN keys per step, as FwdCfg in the dense forward.
-template <int D, int BN, int NT>
+// One 128-row query tile per block and BN keys per step.  TMEM: O in columns
+// [0, D), two S/P buffers behind it, so S of the next step is computed while the
+// softmax works on this one.  At d <= 128 that is 256 columns and about 100 KB of
+// shared memory, and two blocks share an SM: one's start, end and waits lie under
+// the other's work.  (Two tiles per block with 128-key steps, so that a K/V tile
+// serves 256 rows, were 2 to 8% slower on chunks behind up to 16K tokens and 1 to
+// 3% faster behind 32K and more, with query heads sharing tiles; not kept.)
+template <int D, int BN>
 struct PagedCfg {
   static constexpr int kStages = (D == 64) ? 5 : 2;
   static constexpr int kQBytes = kBM * D * 2;
   static constexpr int kKVBytes = BN * D * 2;
   static constexpr int kCols = D / 64;  // 128-byte column blocks
-  static constexpr int kSmemData = NT * kQBytes + 2 * kStages * kKVBytes;
-  static constexpr int kCtas = (NT == 1 && D <= 128) ? 2 : 1;
-  static constexpr int kSmem =
-      kCtas == 2 ? kSmemData + 1024
-                 : (kSmemData + 1024 > 120 * 1024 ? kSmemData + 1024 : 120 * 1024);
-  static constexpr int kSCol0 = NT * D;
+  static constexpr int kSmemData = kQBytes + 2 * kStages * kKVBytes;
+  static constexpr int kCtas = D <= 128 ? 2 : 1;
+  static constexpr int kSmem = kSmemData + 1024;
+  static constexpr int kSCol0 = D;
   static constexpr uint32_t kTmemCols = kCtas == 2 ? 256 : 512;
-  // warp 0: K producer, 1: MMA issuer.  NT = 2: warp 2 V producer, 3 idle,
-  // softmax in warps 4-11.  NT = 1: softmax in warps 2-5, warp 6 V producer.
-  static constexpr int kThreads = NT == 2 ? 384 : 224;
-  static constexpr int kSoftmaxWarp0 = NT == 2 ? 4 : 2;
-  static constexpr int kSoftmaxWarps = 4 * NT;
-  static constexpr int kVWarp = NT == 2 ? 2 : 6;
-  static_assert(NT * D + 2 * BN <= (int)kTmemCols, "TMEM budget");
-  static_assert(kCtas == 1 || 2 * (kSmem + 1024) <= 227 * 1024, "shared memory of two blocks");
+  // warp 0: K producer, 1: MMA issuer, 2-5: softmax, 6: V producer
+  static constexpr int kThreads = 224;
+  static constexpr int kSoftmaxWarp0 = 2;
+  static constexpr int kSoftmaxWarps = 4;
+  static constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
+  static constexpr int kVWarp = 6;
+  static_assert(kJoinRing * 8192 + kJoinWeights * 4 <= kSmemData, "room for join_bulk");
+  static_assert(D + 2 * BN <= (int)kTmemCols, "TMEM budget");
+  static_assert(kCtas == 1 || 2 * (kSmem + 2048) <= 227 * 1024, "shared memory of two blocks");
 };
 
 // One unit of work.
@@ -130,13 +139,14 @@ struct Shapes {
   float work, pairs;  // per head: key steps; tiles
   float long_pairs;   // those of sequences of several tiles
   int longest;        // steps
+  int rows;           // query positions of the largest tile
 };
 // One warp's share, sequences `warp` * 32 + lane and on by `warps` * 32; returns
 // its part of the sums.  raise: report bad lengths.
 __device__ __forceinline__ Shapes gather_shapes(const PagedArgs &a, Shape *at, int warp, int warps,
                                                 int pos, int bn, bool raise) {
   float work = 0.f, pairs = 0.f, long_pairs = 0.f;
-  int longest = 0;
+  int longest = 0, rows = 0;
   for (int i = warp * 32 + (threadIdx.x & 31); i < a.batch; i += warps * 32) {
     const PagedSeq s = paged_seq(a, i);
     if (raise && s.err) raise_error(a.err, s.err);
@@ -146,9 +156,10 @@ __device__ __forceinline__ Shapes gather_shapes(const PagedArgs &a, Shape *at, i
     pairs += (float)x.tiles;
     if (x.tiles > 1) long_pairs += (float)x.tiles;
     longest = max(longest, x.steps);
+    rows = max(rows, min(s.lq, pos));
   }
   return Shapes{at, warp_sum(work), warp_sum(pairs), warp_sum(long_pairs),
-                __reduce_max_sync(0xffffffffu, longest)};
+                __reduce_max_sync(0xffffffffu, longest), __reduce_max_sync(0xffffffffu, rows)};
 }
 
 // x / y for x < 2^24 or so, y > 0 alike in the whole grid: a reciprocal and a
@@ -164,7 +175,7 @@ __device__ __forceinline__ int div_up(int x, int y, float inv_y) {
 // it alike).  pieces(ps): how many items pieces of ps steps make; asked once.
 template <typename F>
 __device__ __forceinline__ int choose_piece(const PagedArgs &a, float work, float pairs,
-                                            int longest, const F &pieces) {
+                                            int longest, int rows, const F &pieces) {
   const float wave = (float)a.wave;
   // least piece that makes about n full ones
   const auto least = [&](float n) {
@@ -173,15 +184,23 @@ __device__ __forceinline__ int choose_piece(const PagedArgs &a, float work, floa
   // Pieces make waves of blocks, and a wave that is started for a few of them
   // is lost.  Pairs of a tile and a head end in a part of a piece, half of one on average: n full
   // pieces make n + pairs / 2.  Take the number of waves whose time -- a piece's
-  // steps, and kBlockSteps for a block's start and end -- is least.  (24 sequences
-  // of 2-9 tokens, d = 64: 2.3 waves 127 us, just below two 109.)
+  // steps, and kBlockSteps for a block's start and end, and the joining of them --
+  // is least.  (24 sequences of 2-9 tokens, d = 64: 2.3 waves 127 us, just below
+  // two 109.)  Of few pairs with many rows the wave need not be full: n pieces of
+  // L steps in all take L / n + join n, least at a piece of sqrt(join L) steps.
+  // (32 tokens, 8 KV heads, behind 4096: 1 piece 45 us, 4 32, 8 36, 16 47.)
+  const float values = (float)(rows * a.pack) * (float)a.d;
+  const float join = values * (1.f / kJoinRate);        // per piece
+  const float join0 = 2.f + values * (1.f / kJoinBase); // once
   int ps = least(2.f * wave);  // more pairs than max_waves hold
   float best = INFINITY, room = 0.f;
   for (int k = 1; k <= a.max_waves; ++k) {
     const float blocks = (float)k * wave;
     if (pairs >= 0.9f * blocks) continue;
-    const int p = least(0.98f * blocks - 0.5f * pairs);
-    const float time = (float)k * (float)(p + kBlockSteps);
+    int p = least(0.98f * blocks - 0.5f * pairs);
+    if (k == 1) p = max(p, (int)sqrtf(join * (float)longest));
+    const float time = (float)k * (float)(p + kBlockSteps) + join0 +
+                       join * __fdividef((float)longest, (float)p);
     if (time < best) {
       best = time;
       ps = p;
@@ -189,7 +208,7 @@ __device__ __forceinline__ int choose_piece(const PagedArgs &a, float work, floa
     }
   }
   // Whole pairs, unless pieces and the joining of them are worth it.
-  if (ceilf(__fdividef(pairs, wave)) * (float)(longest + kBlockSteps) <= best + kJoinSteps)
+  if (ceilf(__fdividef(pairs, wave)) * (float)(longest + kBlockSteps) <= best)
     return INT32_MAX;
   // The average may be off, and the grid has to hold every item.  Where
   // max_waves is 3 it holds all pairs and two waves of full pieces besides; else
@@ -214,7 +233,7 @@ __device__ __forceinline__ bool find_item(const PagedArgs &a, const Shapes &sh, 
   int piece_steps = INT32_MAX;
   float inv_steps = 0.f;
   if (a.num_splits == 0) {
-    piece_steps = choose_piece(a, sh.work * (float)nh, sh.pairs * (float)nh, sh.longest, [&](int ps) {
+    piece_steps = choose_piece(a, sh.work * (float)nh, sh.pairs * (float)nh, sh.longest, sh.rows, [&](int ps) {
       const float inv = __frcp_rn((float)ps);
       float n = (float)first.tiles * (float)div_up(first.steps, ps, inv);
       for (int b0 = 32; b0 < a.batch; b0 += 32) {
@@ -340,9 +359,10 @@ __device__ __forceinline__ Box fetch_boxes(const PagedArgs &a, const Item &it, c
 struct Shared {
   uint64_t q_full;
   uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
-  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t s_full[2], p_full[2], o_done;
   uint64_t v_clean[2];  // first / last V tile: rows that no query sees are zeroed
   uint64_t all_done;    // every MMA of the block has completed
+  uint64_t joined[2];   // groups of pieces have landed
   uint64_t wait_ns;
   Item item;
   Piece piece;
@@ -376,19 +396,19 @@ template <> struct IsBf16<__nv_bfloat16> { static constexpr int v = 1; };
 // for d = 256 four more), asks for the sums and the first kP pieces at once, and
 // has the weights ready in its lanes when the pieces arrive.  (Read past L1:
 // other blocks have written them.)
-template <typename T, int D, int NT, int kWarps, int kR, int kP>
+template <typename T, int D, int kWarps, int kR, int kP>
 __device__ __forceinline__ void join_rows(const PagedArgs &a, const Item &it, int n, int slot0,
                                           int tile_pos, int warp) {
   constexpr int LPR = D / 4 < 32 ? D / 4 : 32;  // lanes of a row
   constexpr int QP = D / 4 / LPR;               // column quads of a lane
   constexpr int RPW = 32 / LPR;                 // rows side by side in a warp
   const int lane = threadIdx.x & 31, sub = lane % LPR, pg = a.pack;
-  const int rows = min(it.s.lq - it.m0, NT * tile_pos) * pg, tile_rows = tile_pos * pg;
+  const int rows = min(it.s.lq - it.m0, tile_pos) * pg;
   const uint32_t inv_pg = (65536 + pg - 1) / pg;  // x / pg = x inv_pg >> 16 for x < 256
-  const int64_t step = (int64_t)it.stride * (NT * kBM);  // rows from a piece to the next
-  const float *l_at = a.lse_part + (int64_t)slot0 * (NT * kBM);
+  const int64_t step = (int64_t)it.stride * kBM;  // rows from a piece to the next
+  const float *l_at = a.lse_part + (int64_t)slot0 * kBM;
   const float4 *o_at = reinterpret_cast<const float4 *>(a.o_part) +
-                       (int64_t)slot0 * (NT * kBM) * (D / 4) + sub;
+                       (int64_t)slot0 * kBM * (D / 4) + sub;
   constexpr int kStep = kWarps * RPW;  // rows from one of a warp's to its next
   for (int x0 = warp * RPW; x0 < rows; x0 += kR * kStep) {
     const int xl = x0 + lane / LPR;
@@ -398,7 +418,7 @@ __device__ __forceinline__ void join_rows(const PagedArgs &a, const Item &it, in
 #pragma unroll
     for (int k = 0; k < kR; ++k) {
       const int x = min(xl + k * kStep, rows - 1);
-      at[k] = x + (NT == 2 && x >= tile_rows ? kBM - tile_rows : 0);
+      at[k] = x;
       l[k] = sub < n ? __ldcg(l_at + at[k] + sub * step) : -INFINITY;
     }
     const auto load = [&](int p0) {
@@ -464,27 +484,123 @@ __device__ __forceinline__ void join_rows(const PagedArgs &a, const Item &it, in
   }
 }
 
-// kCut: keys may be cut into pieces.  (The code that joins them costs the two-tile
-// layout 1.5% in registers of its loop, whether or not it runs.)
-template <typename T, int D, int BN, int NT, bool kCut>
-__global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN, NT>::kCtas)
+// The same for tiles of many rows, where bytes in flight count (join_rows: 8
+// bytes a cycle).  RB rows of a piece lie together in the workspace, 8 KB, and
+// come as one bulk copy; up to kGroup pieces of the same rows make a group, which
+// is waited for and handed back as one (a wait per copy: 11 bytes a cycle), and
+// two groups are in flight or in use.  The weights of all rows and pieces go to
+// shared memory first.  Called by the kThreads softmax threads.
+template <typename T, int D, int kThreads>
+__device__ __forceinline__ void join_bulk(const PagedArgs &a, const Item &it, int n, int slot0,
+                                          int tile_pos, int tid, uint64_t *full, uint8_t *ring) {
+  constexpr int RB = 2048 / D, kTile = RB * D * 4, kQuads = RB * D / 4 / kThreads;
+  constexpr int kGroup = kJoinRing / 2;
+  static_assert(RB * D / 4 % kThreads == 0, "whole quads");
+  float *w = reinterpret_cast<float *>(ring + kJoinRing * kTile);
+  const int pg = a.pack, rows = min(it.s.lq - it.m0, tile_pos) * pg;
+  const uint32_t inv_pg = (65536 + pg - 1) / pg;  // x / pg = x inv_pg >> 16 for x < 256
+  const int64_t step = (int64_t)it.stride * kBM;  // rows from a piece to the next
+  const int batches = (rows + RB - 1) / RB, parts = (n + kGroup - 1) / kGroup;
+  const float *o_at = a.o_part + (int64_t)slot0 * kBM * D;
+  const auto issue = [&](int i) {  // group i; one thread
+    const int b = i / parts, p0 = (i - b * parts) * kGroup, some = min(kGroup, n - p0);
+    const uint32_t bytes = min(RB, rows - b * RB) * D * 4;
+    mbar_expect_tx(&full[i & 1], bytes * some);
+    for (int p = 0; p < some; ++p)
+      bulk_load(ring + ((i & 1) * kGroup + p) * kTile,
+                o_at + ((int64_t)b * RB + (p0 + p) * step) * D, bytes, &full[i & 1]);
+  };
+  if (tid == 0) {
+    fence_async();
+    issue(0);
+    if (batches * parts > 1) issue(1);
+  }
+  for (int x = tid; x < rows; x += kThreads) {
+    const float *l = a.lse_part + (int64_t)slot0 * kBM + x;
+    float m = -INFINITY, sum = 0.f;
+#pragma unroll 4
+    for (int p = 0; p < n; ++p) {
+      const float v = __ldcg(l + p * step);
+      w[x * n + p] = v;
+      m = fmaxf(m, v);
+    }
+    const float ref = m > -INFINITY ? m : 0.f;
+    for (int p = 0; p < n; ++p) {
+      const float e = exp2f(w[x * n + p] - ref);
+      w[x * n + p] = e;
+      sum += e;
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    for (int p = 0; p < n; ++p) w[x * n + p] *= inv;
+    const int p = (int)(x * inv_pg >> 16);
+    const int hr = pg > 1 ? it.head * pg + x - p * pg : it.head;
+    a.lse[(int64_t)hr * a.total_q + it.s.q0 + it.m0 + p] =
+        sum > 0.f ? (ref + log2f(sum)) * kLn2 : -INFINITY;
+  }
+  named_bar_sync(1, kThreads);
+  int i = 0;
+  for (int b = 0; b < batches; ++b) {
+    float o[kQuads][4] = {};
+    const float *wr[kQuads];
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k)
+      wr[k] = w + min(b * RB + (tid + k * kThreads) / (D / 4), rows - 1) * n;
+    for (int p0 = 0; p0 < n; p0 += kGroup, ++i) {
+      // (a copy that never lands raises the error word; all threads go on alike)
+      mbar_wait(&full[i & 1], (i >> 1) & 1, a.err);
+      const float4 *src = reinterpret_cast<const float4 *>(ring + (i & 1) * kGroup * kTile) + tid;
+#pragma unroll
+      for (int p = 0; p < kGroup; ++p) {
+        if (p0 + p < n) {
+#pragma unroll
+          for (int k = 0; k < kQuads; ++k) {
+            const float4 v = src[p * (kTile / 16) + k * kThreads];
+            const float wp = wr[k][p0 + p];
+            o[k][0] = fmaf(wp, v.x, o[k][0]);
+            o[k][1] = fmaf(wp, v.y, o[k][1]);
+            o[k][2] = fmaf(wp, v.z, o[k][2]);
+            o[k][3] = fmaf(wp, v.w, o[k][3]);
+          }
+        }
+      }
+      named_bar_sync(1, kThreads);
+      if (tid == 0 && i + 2 < batches * parts) {
+        fence_async();
+        issue(i + 2);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k) {
+      const int y = tid + k * kThreads, x = b * RB + y / (D / 4);
+      if (x < rows) {
+        const int p = (int)(x * inv_pg >> 16);
+        const int hr = pg > 1 ? it.head * pg + x - p * pg : it.head;
+        const int64_t row = it.s.q0 + it.m0 + p;
+        store_vec<T, 4>(static_cast<T *>(a.o) + (row * a.hq + hr) * D + y % (D / 4) * 4, o[k]);
+      }
+    }
+  }
+}
+
+template <typename T, int D, int BN>
+__global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kCtas)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                     const __grid_constant__ CUtensorMap tv, const PagedArgs a, const int tile_pos,
                     const int box_rows) {
-  using C = PagedCfg<D, BN, NT>;
+  using C = PagedCfg<D, BN>;
   constexpr int ST = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~uintptr_t(1023));
   uint8_t *q_s = smem;
-  uint8_t *k_s = smem + NT * C::kQBytes;
+  uint8_t *k_s = smem + C::kQBytes;
   uint8_t *v_s = k_s + ST * C::kKVBytes;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pg = a.pack;
   // shapes of the sequences: every warp but the one that allocates TMEM
-  Shapes shapes{reinterpret_cast<Shape *>(smem), 0.f, 0.f, 0.f, 0};
+  Shapes shapes{reinterpret_cast<Shape *>(smem), 0.f, 0.f, 0.f, 0, 0};
   constexpr int kGather = C::kThreads / 32 - 1;
   if (warp == 1) {
     tmem_alloc(&sh.tmem_base, C::kTmemCols);
@@ -503,17 +619,18 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
       }
       for (int s = 0; s < 2; ++s) {
         mbar_init(&sh.s_full[s], 1);
-        mbar_init(&sh.o_done[s], 1);
         mbar_init(&sh.v_clean[s], 1);
       }
+      mbar_init(&sh.o_done, 1);
       mbar_init(&sh.all_done, 1);
+      for (int s = 0; s < 2; ++s) mbar_init(&sh.joined[s], 1);
       sh.wait_ns = a.wait_ns;
       sh.abort = 0;
       fence_mbar_init();
     }
     const int w = warp == 0 ? 0 : warp - 1;
     if (w * 32 < a.batch) {
-      const Shapes sum = gather_shapes(a, shapes.at, w, kGather, tile_pos * NT, BN, blockIdx.x == 0);
+      const Shapes sum = gather_shapes(a, shapes.at, w, kGather, tile_pos, BN, blockIdx.x == 0);
       if (lane == 0) sh.sums[w] = sum;
     }
   }
@@ -526,21 +643,19 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
       shapes.pairs += sh.sums[w].pairs;
       shapes.long_pairs += sh.sums[w].long_pairs;
       shapes.longest = max(shapes.longest, sh.sums[w].longest);
+      shapes.rows = max(shapes.rows, sh.sums[w].rows);
     }
     Item it{};
     it.pieces = 1;
-    const bool found = find_item(a, shapes, blockIdx.x, tile_pos * NT, BN, it);
-    const Piece p = piece_of(a, it, tile_pos * NT, BN, found);
+    const bool found = find_item(a, shapes, blockIdx.x, tile_pos, BN, it);
+    const Piece p = piece_of(a, it, tile_pos, BN, found);
     early = fetch_boxes(a, it, p, BN / box_rows, box_rows, p.n_lo * BN, 0);
     if (lane == 0) {
       sh.item = it;
       sh.piece = p;
       // softmax threads that take part: warps with a row of the sequence
-      for (int s = 0; s < 2; ++s) {
-        const int t = NT == 2 ? s : 0;
-        const int rows = min(max(it.s.lq - it.m0 - t * tile_pos, 0), tile_pos) * pg;
-        mbar_init(&sh.p_full[s], max(1, (rows + 31) / 32 * 32));
-      }
+      const int rows = min(max(it.s.lq - it.m0, 0), tile_pos) * pg;
+      for (int s = 0; s < 2; ++s) mbar_init(&sh.p_full[s], max(1, (rows + 31) / 32 * 32));
       fence_mbar_init();
     }
   }
@@ -557,21 +672,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
   const int h = pg > 1 ? kvh * pg : it.head;  // (first) query head of the rows
   const int n_lo = pc.n_lo, nt = pc.nt, front = pc.front, back = pc.back;
   const bool live = pc.live;
-  // steps [ta, tb) of the piece that tile t takes part in: those with a key
-  // that one of its rows sees
-  auto tile_steps = [&](int t, int &ta, int &tb) {
-    ta = 0;
-    tb = nt;
-    if constexpr (NT == 2) {
-      const Steps x = key_steps(a, sq, it.m0 + t * tile_pos, tile_pos, BN);
-      ta = min(max(x.n_lo - n_lo, 0), nt);
-      tb = min(max(x.n_lo + x.nt - n_lo, ta), nt);
-      if (x.nt == 0) ta = tb = 0;
-    }
-  };
-
   if (warp < C::kSoftmaxWarp0 || warp >= C::kSoftmaxWarp0 + C::kSoftmaxWarps) {
-    if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
     if (warp == 0 || warp == C::kVWarp) {
       // ----------------------------------------- producers: warp 0 K, kVWarp V
       if (nt > 0) {
@@ -584,11 +685,9 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
         uint8_t *dst = (is_v ? v_s : k_s) + col * (BN * 128) + box * box_rows * 128;
         Box now{-1, 0}, ahead = is_v ? fetch_boxes(a, it, pc, boxes, box_rows, key_lo, 0) : early;
         if (!is_v && lane == 0) {
-          mbar_expect_tx(&sh.q_full, NT * tile_pos * pg * D * 2);
-          for (int t = 0; t < NT; ++t)
-            for (int c = 0; c < C::kCols; ++c)
-              tma_load_3d(q_s + t * C::kQBytes + c * kBM * 128, &tq, &sh.q_full, c * 64, h,
-                          sq.q0 + it.m0 + t * tile_pos);
+          mbar_expect_tx(&sh.q_full, tile_pos * pg * D * 2);
+          for (int c = 0; c < C::kCols; ++c)
+            tma_load_3d(q_s + c * kBM * 128, &tq, &sh.q_full, c * 64, h, sq.q0 + it.m0);
         }
         // zeroes rows [r0, r1) of V tile j once it has landed
         auto clean = [&](int j, int r0, int r1, uint64_t *bar) {
@@ -653,23 +752,27 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
         const uint64_t q_d = smem_desc(smem_u32(q_s), 16, 1024);
         const uint64_t k_d = smem_desc(smem_u32(k_s), 16, 1024);
         const uint64_t v_d = smem_desc(smem_u32(v_s), BN * 128, 1024);
-        auto mma_s = [&](int t, int j, uint32_t dcol) {
+        auto mma_s = [&](int j) {  // S_j = Q K_j^T
           const uint32_t ko = (j % ST) * C::kKVBytes;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t ad =
-                desc_add(q_d, t * C::kQBytes + (kk / 4) * (kBM * 128) + (kk % 4) * 32);
+            const uint64_t ad = desc_add(q_d, (kk / 4) * (kBM * 128) + (kk % 4) * 32);
             const uint64_t bd = desc_add(k_d, ko + (kk / 4) * (BN * 128) + (kk % 4) * 32);
-            mma_ss(dcol, ad, bd, id_s, kk > 0);
+            mma_ss(tmem + C::kSCol0 + (j & 1) * BN, ad, bd, id_s, kk > 0);
           }
+          mma_commit(&sh.s_full[j & 1]);
+          mma_commit(&sh.k_empty[j % ST]);
         };
-        auto mma_pv = [&](int t, int j, uint32_t pcol, bool first) {
+        auto mma_pv = [&](int j) {  // O (+)= P_j V_j
           const uint32_t vo = (j % ST) * C::kKVBytes;
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk) {
             const uint64_t bd = desc_add(v_d, vo + kk * 16 * 128);
-            mma_ts(tmem + t * D, pcol + kk * 8, bd, id_o, (!first || kk > 0) ? 1u : 0u);
+            mma_ts(tmem, tmem + C::kSCol0 + (j & 1) * BN + kk * 8, bd, id_o,
+                   (j > 0 || kk > 0) ? 1u : 0u);
           }
+          mma_commit(&sh.o_done);
+          mma_commit(&sh.v_empty[j % ST]);
         };
         auto k_ready = [&](int j) {
           const bool r = wait_bar(sh, &sh.k_full[j % ST], (j / ST) & 1, a.err);
@@ -683,78 +786,20 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
           tc_fence_after();
           return r;
         };
-        int ta[NT], tb[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) tile_steps(t, ta[t], tb[t]);
         // test hook: all_done completes only after this thread's last commit
-        const bool stalled = a.stall && !wait_bar(sh, &sh.all_done, 0, a.err);
-        if (stalled) {
-        } else if (NT == 2) {
-          // S_0(0) S_1(0) | PV_0(j) S_0(j+1) PV_1(j) S_1(j+1) | ..., where a
-          // tile takes part in step j only inside its own range; every K and V
-          // tile is waited for once before its stage is released
-          bool ok = nt == 0 || (wait_bar(sh, &sh.q_full, 0, a.err) && k_ready(0));
-          if (ok && nt > 0) {
-            for (int t = 0; t < NT; ++t) {
-              if (ta[t] == 0 && tb[t] > 0) {
-                mma_s(t, 0, tmem + C::kSCol0 + t * BN);
-                mma_commit(&sh.s_full[t]);
-              }
-            }
-            mma_commit(&sh.k_empty[0]);
+        bool ok = !(a.stall && !wait_bar(sh, &sh.all_done, 0, a.err));
+        // S(0) | S(j+1) PV(j) | ...
+        ok = ok && (nt == 0 || (wait_bar(sh, &sh.q_full, 0, a.err) && k_ready(0)));
+        if (ok && nt > 0) mma_s(0);
+        for (int j = 0; ok && j < nt; ++j) {
+          if (j + 1 < nt) {
+            if (!k_ready(j + 1)) break;
+            mma_s(j + 1);
           }
-          for (int j = 0; ok && j < nt; ++j) {
-            const bool k_next = j + 1 < nt;
-            const int last_pv = (j >= ta[1] && j < tb[1]) ? 1 : 0;
-            const int last_s = (j + 1 >= ta[1] && j + 1 < tb[1]) ? 1 : 0;
-            bool v_in = false, k_in = false;
-            for (int t = 0; t < NT && ok; ++t) {
-              const uint32_t scol = tmem + C::kSCol0 + t * BN;
-              if (j >= ta[t] && j < tb[t]) {
-                if (!wait_bar(sh, &sh.p_full[t], (j - ta[t]) & 1, a.err)) { ok = false; break; }
-                tc_fence_after();
-                if (!v_in && !(v_in = v_ready(j))) { ok = false; break; }
-                mma_pv(t, j, scol, j == ta[t]);
-                mma_commit(&sh.o_done[t]);
-                if (t == last_pv) mma_commit(&sh.v_empty[j % ST]);
-              }
-              if (k_next && j + 1 >= ta[t] && j + 1 < tb[t]) {
-                if (!k_in && !(k_in = k_ready(j + 1))) { ok = false; break; }
-                mma_s(t, j + 1, scol);
-                mma_commit(&sh.s_full[t]);
-                if (t == last_s) mma_commit(&sh.k_empty[(j + 1) % ST]);
-              }
-            }
-            if (ok && !v_in) {
-              if (!v_ready(j)) break;
-              mma_commit(&sh.v_empty[j % ST]);
-            }
-            if (ok && k_next && !k_in) {
-              if (!k_ready(j + 1)) break;
-              mma_commit(&sh.k_empty[(j + 1) % ST]);
-            }
-          }
-        } else {
-          bool ok = nt == 0 || (wait_bar(sh, &sh.q_full, 0, a.err) && k_ready(0));
-          if (ok && nt > 0) {
-            mma_s(0, 0, tmem + C::kSCol0);
-            mma_commit(&sh.s_full[0]);
-            mma_commit(&sh.k_empty[0]);
-          }
-          for (int j = 0; ok && j < nt; ++j) {
-            if (j + 1 < nt) {
-              if (!k_ready(j + 1)) break;
-              mma_s(0, j + 1, tmem + C::kSCol0 + ((j + 1) & 1) * BN);
-              mma_commit(&sh.s_full[(j + 1) & 1]);
-              mma_commit(&sh.k_empty[(j + 1) % ST]);
-            }
-            if (!wait_bar(sh, &sh.p_full[j & 1], (j >> 1) & 1, a.err)) break;
-            tc_fence_after();
-            if (!v_ready(j)) break;
-            mma_pv(0, j, tmem + C::kSCol0 + (j & 1) * BN, j == 0);
-            mma_commit(&sh.o_done[0]);
-            mma_commit(&sh.v_empty[j % ST]);
-          }
+          if (!wait_bar(sh, &sh.p_full[j & 1], (j >> 1) & 1, a.err)) break;
+          tc_fence_after();
+          if (!v_ready(j)) break;
+          mma_pv(j);
         }
         // after an abort, no MMA may still run when the TMEM is released
         mma_commit(&sh.all_done);
@@ -765,17 +810,15 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
       }
     }
   } else {
-    if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
     // ------------------------------------------------------------ softmax
-    const int t = (warp - C::kSoftmaxWarp0) >> 2;  // query tile of this warpgroup
     const int r0 = 32 * (warp & 3), r = r0 + lane;  // TMEM lane = row in the tile
-    const int first = it.m0 + t * tile_pos;         // the tile's first query position
+    const int first = it.m0;                        // the tile's first query position
     const int rows = min(max(sq.lq - first, 0), tile_pos) * pg;  // its rows in the sequence
     if (live && r0 < rows) {
       const int i = first + r / pg;  // query position
       const int hr = h + r % pg;     // and query head
       const uint32_t lane_off = (uint32_t)r0 << 16;
-      const uint32_t o_t = tmem + lane_off + t * D;
+      const uint32_t o_t = tmem + lane_off;
       int lo_i, hi_i;
       key_range(i, sq.lq, sq.lk, a.win_l, a.win_r, lo_i, hi_i);
       const uint32_t n_vis = (uint32_t)max(hi_i - lo_i + 1, 0);  // keys this row sees
@@ -791,14 +834,10 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
       const float cap_k = cap_in * 2.8853900817779268f;  // 2 log2(e) cap_in
       float m_ref = -INFINITY, l = 0.f;
       bool ok = true;
-      int ta, tb;
-      tile_steps(t, ta, tb);
-      const int ntt = tb - ta;
-      for (int j = 0; j < ntt; ++j) {
-        const int key0 = (n_lo + ta + j) * BN;
-        const int sb = NT == 2 ? t : (j & 1);  // S/P buffer and its barriers
-        const uint32_t s_par = NT == 2 ? (j & 1) : ((j >> 1) & 1);
-        if (!wait_warp(sh, &sh.s_full[sb], s_par, a.err)) { ok = false; break; }
+      for (int j = 0; j < nt; ++j) {
+        const int key0 = (n_lo + j) * BN;
+        const int sb = j & 1;  // S/P buffer and its barriers
+        if (!wait_warp(sh, &sh.s_full[sb], (j >> 1) & 1, a.err)) { ok = false; break; }
         tc_fence_after();
         const uint32_t scol = tmem + lane_off + C::kSCol0 + sb * BN;
         float x[BN];
@@ -901,7 +940,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
           // rescaled.  (Without a rescale there is nothing to wait for: P_j has
           // its own columns, and the product that reads it is issued later.  The
           // parity cannot be mistaken: step j's product needs this warp's P.)
-          if (!wait_warp(sh, &sh.o_done[t], (j - 1) & 1, a.err)) { ok = false; break; }
+          if (!wait_warp(sh, &sh.o_done, (j - 1) & 1, a.err)) { ok = false; break; }
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -917,8 +956,8 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
         tc_fence_before();
         mbar_arrive(&sh.p_full[sb]);
       }
-      // epilogue.  all_done, not the tile's own last step: a page outside the
-      // pool anywhere in the piece then empties both tiles, every run alike.
+      // epilogue.  (Also after an abort: a page outside the pool leaves the result
+      // of no keys, every run alike.)
       ok = __all_sync(0xffffffffu, ok && wait_bar(sh, &sh.all_done, 0, a.err) &&
                                        !*(volatile int *)&sh.abort);
       tc_fence_after();
@@ -927,11 +966,11 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
       const float lse2 = l > 0.f ? (m_ref == -INFINITY ? 0.f : m_ref) + __log2f(l) : -INFINITY;
       const bool valid = r < rows;
       T *orow = static_cast<T *>(a.o) + ((int64_t)(sq.q0 + i) * a.hq + hr) * D;
-      const int64_t part = (int64_t)it.slot * (NT * kBM) + t * kBM + r;
+      const int64_t part = (int64_t)it.slot * kBM + r;
 #pragma unroll 1
       for (int c2 = 0; c2 < D / 64; ++c2) {
         uint32_t u[64];
-        if (ok && ntt > 0) {
+        if (ok && nt > 0) {
           tmem_ld32(o_t + c2 * 64, *reinterpret_cast<uint32_t(*)[32]>(u));
           tmem_ld32(o_t + c2 * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(u + 32));
           tmem_wait_ld();
@@ -939,7 +978,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
 #pragma unroll
           for (int e = 0; e < 64; ++e) u[e] = 0u;
         }
-        if (!kCut || it.pieces == 1) {
+        if (it.pieces == 1) {
           uint32_t w[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e)
@@ -950,7 +989,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
             for (int e = 0; e < 8; ++e)
               dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
           }
-        } else if (kCut && valid && it.slot < a.slots) {
+        } else if (valid && it.slot < a.slots) {
           float4 *dst = reinterpret_cast<float4 *>(a.o_part + part * D + c2 * 64);
 #pragma unroll
           for (int e = 0; e < 16; ++e)
@@ -960,19 +999,19 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
         }
       }
       if (valid) {
-        if (!kCut || it.pieces == 1)
+        if (it.pieces == 1)
           a.lse[(int64_t)hr * a.total_q + sq.q0 + i] = lse2 * kLn2;
         else if (it.slot < a.slots)
           a.lse_part[part] = lse2;
       }
-      if (kCut && it.pieces > 1) __threadfence();  // before the piece is counted as written
+      if (it.pieces > 1) __threadfence();  // before the piece is counted as written
     }
     // The block that writes the last piece of a pair joins them (its softmax
     // warps, which have the registers for it; every copy and product of the
     // block has completed, so the tiles' space is free).
     // (the item is read again from shared memory: registers are short above)
-    if (kCut && live && reinterpret_cast<volatile int &>(sh.item.pieces) > 1) {
-      named_bar_sync(1, 128 * NT);
+    if (live && reinterpret_cast<volatile int &>(sh.item.pieces) > 1) {
+      named_bar_sync(1, C::kSoftmaxThreads);
       const Item jt = sh.item;
       const int n = sh.piece.written;
       const int slot0 = jt.slot - jt.piece * jt.stride;  // of the first piece
@@ -983,13 +1022,18 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, NT>::kThreads, PagedCfg<D, BN,
         sh.joins = fits && atomicAdd(&a.written[slot0], 1) == n - 1;
         __threadfence();
       }
-      named_bar_sync(1, 128 * NT);
+      named_bar_sync(1, C::kSoftmaxThreads);
       if (sh.joins) {
-        // few rows (single tokens): many pieces at a time; else many rows
-        if (min(jt.s.lq - jt.m0, NT * tile_pos) * a.pack <= 4 * C::kSoftmaxWarps)
-          join_rows<T, D, NT, C::kSoftmaxWarps, 1, 4>(a, jt, n, slot0, tile_pos, tid >> 5);
+        // Few rows (single tokens): a warp per row, many pieces at a time.  Many:
+        // through shared memory, if the weights fit beside the ring, and if no
+        // copy of an abandoned piece may still be landing there.
+        const int rows = min(jt.s.lq - jt.m0, tile_pos) * a.pack;
+        if (rows <= 4 * C::kSoftmaxWarps)
+          join_rows<T, D, C::kSoftmaxWarps, 1, 4>(a, jt, n, slot0, tile_pos, tid >> 5);
+        else if (rows * n <= kJoinWeights && !*(volatile int *)&sh.abort)
+          join_bulk<T, D, C::kSoftmaxThreads>(a, jt, n, slot0, tile_pos, tid, sh.joined, smem);
         else
-          join_rows<T, D, NT, C::kSoftmaxWarps, 2, 4>(a, jt, n, slot0, tile_pos, tid >> 5);
+          join_rows<T, D, C::kSoftmaxWarps, 2, 4>(a, jt, n, slot0, tile_pos, tid >> 5);
       }
     }
   }
@@ -1024,9 +1068,9 @@ bool make_pool_map(CUtensorMap *m, const void *base, const PagedArgs &a, int64_t
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int D, int BN, int NT, bool kCut = true>
+template <typename T, int D, int BN>
 cudaError_t paged(const PagedArgs &a, const PagedPlan &plan, cudaStream_t st) {
-  using C = PagedCfg<D, BN, NT>;
+  using C = PagedCfg<D, BN>;
   // a box never leaves its page
   const int box_rows = a.block_table ? std::gcd(a.page_size, BN) : BN;
   CUtensorMap tq, tk, tv;
@@ -1034,13 +1078,11 @@ cudaError_t paged(const PagedArgs &a, const PagedPlan &plan, cudaStream_t st) {
       !make_pool_map(&tk, a.k_cache, a, a.k_ps, box_rows) ||
       !make_pool_map(&tv, a.v_cache, a, a.v_ps, box_rows))
     return cudaErrorInvalidValue;
-  cudaError_t e = set_smem_once<paged_tc_kernel<T, D, BN, NT, kCut>>(C::kSmem);
-  if (e == cudaSuccess && NT == 2)  // 128 * 88 + 256 * 208 after setmaxnreg
-    e = check_regs_once<paged_tc_kernel<T, D, BN, NT, kCut>>(C::kThreads, 128 * 88 + 256 * 208);
+  cudaError_t e = set_smem_once<paged_tc_kernel<T, D, BN>>(C::kSmem);
   if (e != cudaSuccess) return e;
-  debug_log("paged: paged_tc_kernel d=%d, %d query tile(s) of 128 rows per block, %d-key tiles in "
-            "boxes of %d, pack=%d, num_splits=%d (wave %d), grid=%lld x %d threads, smem=%d B",
-            D, NT, BN, box_rows, a.pack, a.num_splits, a.wave, (long long)plan.items, C::kThreads,
+  debug_log("paged: paged_tc_kernel d=%d, %d-key tiles in boxes of %d, pack=%d, num_splits=%d "
+            "(wave %d), grid=%lld x %d threads, smem=%d B",
+            D, BN, box_rows, a.pack, a.num_splits, a.wave, (long long)plan.items, C::kThreads,
             C::kSmem);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)plan.items);
@@ -1056,7 +1098,7 @@ cudaError_t paged(const PagedArgs &a, const PagedPlan &plan, cudaStream_t st) {
     count_launches(1);
     cfg.numAttrs = 1;
   }
-  e = cudaLaunchKernelEx(&cfg, paged_tc_kernel<T, D, BN, NT, kCut>, tq, tk, tv, a, plan.tile_pos, box_rows);
+  e = cudaLaunchKernelEx(&cfg, paged_tc_kernel<T, D, BN>, tq, tk, tv, a, plan.tile_pos, box_rows);
   if (e != cudaSuccess) return e;
   count_launches(1);
   return cudaGetLastError();
@@ -1064,28 +1106,28 @@ cudaError_t paged(const PagedArgs &a, const PagedPlan &plan, cudaStream_t st) {
 
 }  // namespace
 
+constexpr int kKeysPerStep = 64;
+
 PagedPlan paged_plan(int batch, int total_q, int hq, int hkv, int d, int num_splits, int64_t keys,
                      int sms) {
   PagedPlan p{};
   const int g = hq / hkv;
   // The g query heads of a KV head share tiles: K and V are then read once for
-  // all of them.  Not where their rows fill less than three quarters of a tile
-  // (g = 44 .. 95 or above 128 leaves 128 % g rows empty) and the chunks are long
-  // enough to fill tiles of one head.
+  // all of them.  Not where their rows fill less than seven eighths of a tile and
+  // the chunks fill tiles of one head.  (One KV head, 2048 cached tokens: g = 48,
+  // 96 of 128 rows, chunks of 64 143 us shared and 185 apart, of 256 144 and 112;
+  // g = 64, all rows, 148 and 230, 148 and 141.)
   const int used = g <= 128 ? 128 / g * g : 0;
-  p.pack = used >= 96 || (used > 0 && total_q < 64 * (int64_t)batch) ? g : 1;
+  p.pack = used >= 112 || (used > 0 && total_q < 96 * (int64_t)batch) ? g : 1;
   p.tile_pos = kBM / p.pack;
-  // two tiles per block (every K/V tile then serves 256 rows) where the
-  // average sequence fills two such blocks
-  p.layout = d == 128 && (int64_t)total_q * p.pack >= 512 * (int64_t)batch ? 2 : 1;
   const int nh = p.pack > 1 ? hkv : hq;
-  const int pos = p.tile_pos * p.layout;
-  const int64_t wave = (int64_t)sms * (p.layout == 1 && d <= 128 ? 2 : 1);
+  const int64_t wave = (int64_t)sms * (d <= 128 ? 2 : 1);
   // sum of ceil(n_i / pos) over sequences of sum total_q
-  p.tiles = (total_q / pos + std::min(batch, total_q)) * (int64_t)nh;
+  p.tiles = (total_q / p.tile_pos + std::min(batch, total_q)) * (int64_t)nh;
   p.num_splits = std::min(num_splits, kMaxSplits);
   // enough tiles for several waves even if no sequence leaves one half empty
-  if (num_splits == 0 && (int64_t)(total_q + pos - 1) / pos * nh >= 4 * wave) p.num_splits = 1;
+  if (num_splits == 0 && (int64_t)(total_q + p.tile_pos - 1) / p.tile_pos * nh >= 4 * wave)
+    p.num_splits = 1;
   p.wave = (int)wave;
   if (p.num_splits == 0) {
     // few pairs divide evenly into one wave; many leave ragged pieces, which
@@ -1098,31 +1140,28 @@ PagedPlan paged_plan(int batch, int total_q, int hq, int hkv, int d, int num_spl
     if (p.max_waves == 3) p.items = std::max(p.items, p.tiles + 2 * wave);
     p.slots = std::min(4 * wave, p.items);
     // short caches: a pair cannot make more pieces than this
-    const int64_t steps = keys / (p.layout == 2 ? 128 : 64) + 2;
+    const int64_t steps = keys / kKeysPerStep + 2;
     p.items = std::min(p.items, p.tiles * ((steps + kMinPieceSteps - 1) / kMinPieceSteps));
   } else {
     p.items = p.tiles * p.num_splits;
     p.slots = p.num_splits > 1 ? p.items : 0;
   }
   // partial O and log2-sums, and a count of written pieces per slot
-  p.ws_bytes = (size_t)p.slots * (kBM * p.layout * (d + 1) * sizeof(float) + sizeof(int));
+  p.ws_bytes = (size_t)p.slots * (kBM * (d + 1) * sizeof(float) + sizeof(int));
   return p;
 }
 
+template <int D>
+static cudaError_t paged_d(const PagedArgs &a, const PagedPlan &plan, cudaStream_t st) {
+  return a.dtype == ATTN_BF16 ? paged<__nv_bfloat16, D, kKeysPerStep>(a, plan, st)
+                              : paged<__half, D, kKeysPerStep>(a, plan, st);
+}
+
 cudaError_t launch_paged_tc(const PagedArgs &a, const PagedPlan &plan, cudaStream_t st) {
-  const bool bf = a.dtype == ATTN_BF16;
   switch (a.d) {
-    case 64:
-      return bf ? paged<__nv_bfloat16, 64, 64, 1>(a, plan, st) : paged<__half, 64, 64, 1>(a, plan, st);
-    case 128:
-      if (plan.layout == 2 && plan.num_splits == 1)
-        return bf ? paged<__nv_bfloat16, 128, 128, 2, false>(a, plan, st)
-                  : paged<__half, 128, 128, 2, false>(a, plan, st);
-      if (plan.layout == 2)
-        return bf ? paged<__nv_bfloat16, 128, 128, 2>(a, plan, st) : paged<__half, 128, 128, 2>(a, plan, st);
-      return bf ? paged<__nv_bfloat16, 128, 64, 1>(a, plan, st) : paged<__half, 128, 64, 1>(a, plan, st);
-    case 256:
-      return bf ? paged<__nv_bfloat16, 256, 64, 1>(a, plan, st) : paged<__half, 256, 64, 1>(a, plan, st);
+    case 64: return paged_d<64>(a, plan, st);
+    case 128: return paged_d<128>(a, plan, st);
+    case 256: return paged_d<256>(a, plan, st);
   }
   return cudaErrorInvalidValue;
 }
