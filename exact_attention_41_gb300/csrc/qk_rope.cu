@@ -324,7 +324,8 @@ __device__ __forceinline__ void bwd_kind(const RopeArgs &a, const T *x, const T 
       float xh[16], wv[16];
       widen<T>(x_now, xh);
       widen<T>(wr, wv);
-      const float r = inv_rms<D>(xh, a.eps);
+      const float rms = inv_rms<D>(xh, a.eps);
+      const float r = h0 < heads ? rms : 0.f;  // (no head here: infinite where eps is 0)
       float dot = 0.f;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {

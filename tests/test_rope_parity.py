@@ -245,6 +245,33 @@ def test_in_place_and_packed_views():
     assert torch.equal(g3[1], g2[1]) and g3[1].data_ptr() == gq2.data_ptr()
 
 
+@pytest.mark.parametrize("hkv,d", [(1, 128), (3, 64), (1, 256)])
+def test_gradient_without_epsilon(hkv, d):
+    """eps = 0 with heads that leave lanes of a warp without one: their empty
+    rows have no finite 1 / rms, which must not reach the weight's gradient."""
+    import torch
+
+    from exact_attention_41_gb300 import libattn
+
+    dtype, b, s = syn.BF16, 2, 21
+    rng, _, k = case_data(8, b, s, 1, hkv, d, dtype)
+    gk = syn.normal_bits(rng, (b, s, hkv, d), dtype)
+    w, w64 = weights(rng, d, dtype)
+    _, dk, _, dw = libattn.qk_norm_rope_bwd(None, dev(k, dtype), None, dev(gk, dtype),
+                                            phases=phases(d), k_weight=w, eps=0.0)
+    torch.cuda.synchronize()
+    x, gy = (f64(t, dtype).reshape(b * s, hkv, d) for t in (k, gk))
+    at = np.broadcast_to(np.arange(s), (b, s)).reshape(-1)
+    want, want_w = serving.norm_rope_backward(x, gy, at, freqs(d), w64, 0.0)
+    gz = serving.rotate(gy, -at, freqs(d))
+    r = 1 / np.sqrt((x * x).mean(-1, keepdims=True))
+    big = r * np.abs(w64).max() * np.abs(gz).max(-1, keepdims=True) * \
+        (1 + np.abs(x * r).max(-1, keepdims=True))
+    check(host(dk).reshape(want.shape), want, HALF[dtype] * np.abs(want) + 128 * U * big + TINY, "dk")
+    check(host(dw), want_w, HALF[dtype] * np.abs(want_w) +
+          (b * s * hkv + 160) * U * np.abs(gz * x * r).reshape(-1, d).sum(0) + TINY, "dw")
+
+
 def test_empty_training_batch_has_zero_weight_gradients():
     import torch
 
