@@ -141,6 +141,13 @@ def _stream():
     return _raw_stream(torch.cuda.current_device())
 
 
+def _int(x):
+    """x as a C int, the nearest one where it is out of range (ctypes would cut
+    its upper bits off: a window of 2^32 would become one of 0)."""
+    x = int(x)
+    return x if -0x80000000 <= x < 0x80000000 else 0x7fffffff if x > 0 else -0x80000000
+
+
 def _need(cond, msg):
     if not cond:
         raise ValueError(msg)
@@ -173,6 +180,7 @@ def _row_stride(t):
     _need(t.stride(3) == 1 and t.stride(2) == d and (b == 1 or t.stride(0) == s * t.stride(1)),
           "a non-contiguous q/k/v must be a token-strided view with dense heads "
           "(e.g. of a packed (b, s, 3, h, d) tensor)")
+    _need(t.stride(1) > 0, "a tensor expanded over its tokens has no rows of its own")
     return t.stride(1)
 
 
@@ -481,6 +489,7 @@ def _packed_stride(t):
     rows, h, d = t.shape
     _need(t.stride(2) == 1 and (h == 1 or t.stride(1) == d),
           "a non-contiguous q/k/v must be a token-strided view with dense heads")
+    _need(rows <= 1 or t.stride(0) > 0, "a tensor expanded over its rows has none of its own")
     return 0 if rows <= 1 else t.stride(0)
 
 
@@ -492,6 +501,7 @@ def _page_stride(t):
     n, ps, h, d = t.shape
     _need(t.stride(3) == 1 and (h == 1 or t.stride(2) == d) and (ps == 1 or t.stride(1) == h * d),
           "the pages of a cache must be dense; only the page stride may be larger")
+    _need(n <= 1 or t.stride(0) > 0, "a cache expanded over its pages has none of its own")
     return 0 if n <= 1 else t.stride(0)
 
 
@@ -521,7 +531,7 @@ def paged_workspace(q, k_cache, batch, num_splits=0):
     _need(q.is_cuda, "tensors must be on a CUDA device")
     with torch.cuda.device(q.device):
         n = lib().attn_fwd_paged_workspace_size(int(batch), rows, hq, k_cache.shape[2], d,
-                                                int(num_splits))
+                                                _int(num_splits))
     return torch.empty(max(n, 1), device=q.device, dtype=torch.uint8)
 
 
@@ -555,8 +565,8 @@ def fwd_paged(q, k_cache, v_cache, cu_seqlens_q, cache_seqlens, *, block_table=N
            _packed_stride(q), _page_stride(k_cache), _page_stride(v_cache),
            cu_seqlens_q.data_ptr(), cache_seqlens.data_ptr(), _p(block_table), num_pages,
            page_size, max_pages, 1 if appended else 0, batch, rows, _dt(q), hq, hkv, d,
-           d ** -0.5 if scale is None else scale, 1 if causal else 0, int(wl), int(wr), softcap,
-           num_splits, workspace.data_ptr(), workspace.nbytes),
+           d ** -0.5 if scale is None else scale, 1 if causal else 0, _int(wl), _int(wr),
+           softcap, _int(num_splits), workspace.data_ptr(), workspace.nbytes),
           (out, lse, cu_seqlens_q, cache_seqlens, block_table, workspace),
           (q, k_cache, v_cache))
     return out, lse

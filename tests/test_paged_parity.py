@@ -153,6 +153,12 @@ def test_windows_wider_than_any_sequence():
     run(c, causal=True, window=(big, 0))
 
 
+def test_windows_wider_than_a_c_int():
+    c = make(14, [40, 1, 7], [100, 300, 0], 4, 2, 64, 16, syn.F16)
+    run(c, window=(2 ** 32, 2 ** 40))
+    run(c, causal=True, window=(2 ** 32 + 5, 0), num_splits=2 ** 33)
+
+
 def test_many_sequences():
     """More sequences than a warp has lanes, most of one token, some empty."""
     rng = np.random.default_rng(5)

@@ -153,3 +153,39 @@ def test_binding_refusals():
         libattn.fwd_paged(q[0], pool, pool, cu, cs)
     with pytest.raises(ValueError, match="CUDA"):
         libattn.kvcache_append(q[0], q[0], pool, pool, cu, cs)
+
+
+def test_expanded_tensors_are_refused():
+    """A stride of 0 stands for contiguous rows in the C calls: an expanded
+    tensor, which has it, would be read past its end."""
+    torch = pytest.importorskip("torch")
+    row = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="expanded"):
+        libattn._packed_stride(row.expand(4, 2, 64))
+    assert libattn._packed_stride(row) == 0
+    page = torch.zeros(1, 16, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="expanded"):
+        libattn._page_stride(page.expand(4, 16, 2, 64))
+    assert libattn._page_stride(page) == 0
+    wide = torch.zeros(4, 3, 2, 64, dtype=torch.bfloat16)
+    assert libattn._packed_stride(wide[:, 0]) == 3 * 2 * 64
+
+    class OnDevice:  # the layout of a CUDA tensor, without one
+        is_cuda, shape = True, (1, 4, 2, 64)
+
+        def is_contiguous(self):
+            return False
+
+        def stride(self, i):
+            return (0, 0, 64, 1)[i]
+
+    with pytest.raises(ValueError, match="expanded"):
+        libattn._row_stride(OnDevice())
+
+
+def test_numbers_beyond_a_c_int():
+    import sys
+
+    for x, want in ((2 ** 32, 2 ** 31 - 1), (sys.maxsize, 2 ** 31 - 1), (-2 ** 40, -2 ** 31), (-1, -1),
+                    (2 ** 31 - 1, 2 ** 31 - 1), (-2 ** 31, -2 ** 31)):
+        assert libattn._int(x) == want
