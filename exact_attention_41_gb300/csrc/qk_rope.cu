@@ -150,8 +150,9 @@ __device__ __forceinline__ Token find_token(const RopeArgs &a, int r) {
   }
   if (seq >= a.batch) return tk;  // behind the last sequence
   const int first = a.cu_seqlens[seq];
+  const int end = a.cu_seqlens[seq + 1];
   const int cached = a.cache_seqlens[seq];
-  if (first < 0 || r < first || cached < 0) {
+  if (first < 0 || r < first || r >= end || cached < 0) {
     if (lane == 0) raise_error(a.err, kErrBadSeqlen);
     return tk;
   }

@@ -397,6 +397,22 @@ def test_append_bad_pages_and_lengths():
             assert torch.equal(vc[pg, sl], ref[pg, sl]), (bit, r)
 
 
+def test_append_offsets_out_of_order():
+    """Offsets that decrease: flagged, and a token is written by the sequence
+    whose range holds it or not at all (row 3 lies in none but the broken one)."""
+    from exact_attention_41_gb300 import libattn
+
+    new, cached = [9, 0, 1, 2], [0, 0, 0, 5]
+    c = append_data(24, new, cached, 2, 1, 64, 16, syn.F16, pad=0)
+    c["cu"] = np.asarray([0, 9, 1, 2, 12], np.int32)
+    libattn.device_error()
+    kc, vc, _ = libattn_append(c, syn.F16, cached)
+    assert libattn.device_error() == (6, 16)
+    before = dev(c["vc"], syn.F16)
+    third = c["table"][2, 0]
+    assert (vc[third] == before[third]).all()
+
+
 def _with(table, at, value):
     t = table.copy()
     t[at] = value
