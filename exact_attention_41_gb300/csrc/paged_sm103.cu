@@ -1037,6 +1037,8 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
       }
     }
   }
+  // this grid, and with it the call, does not end before paged_zero_kernel
+  if (blockIdx.x == 0 && threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
@@ -1123,10 +1125,10 @@ PagedPlan paged_plan(int batch, int total_q, int hq, int hkv, int d, int num_spl
   const int nh = p.pack > 1 ? hkv : hq;
   const int64_t wave = (int64_t)sms * (d <= 128 ? 2 : 1);
   // sum of ceil(n_i / pos) over sequences of sum total_q
-  p.tiles = (total_q / p.tile_pos + std::min(batch, total_q)) * (int64_t)nh;
+  p.tiles = ((int64_t)total_q / p.tile_pos + std::min(batch, total_q)) * nh;
   p.num_splits = std::min(num_splits, kMaxSplits);
   // enough tiles for several waves even if no sequence leaves one half empty
-  if (num_splits == 0 && (int64_t)(total_q + p.tile_pos - 1) / p.tile_pos * nh >= 4 * wave)
+  if (num_splits == 0 && ((int64_t)total_q + p.tile_pos - 1) / p.tile_pos * nh >= 4 * wave)
     p.num_splits = 1;
   p.wave = (int)wave;
   if (p.num_splits == 0) {
