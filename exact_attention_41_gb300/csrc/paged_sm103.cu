@@ -37,8 +37,8 @@
 #include <algorithm>
 #include <numeric>
 
+#include "copies.cuh"
 #include "paged.cuh"
-#include "sm103.cuh"
 
 namespace attn {
 namespace {

@@ -23,8 +23,8 @@
 // Everything is held in fp32 and rounded once, to the output.
 #include <algorithm>
 
+#include "copies.cuh"
 #include "kernels.h"
-#include "sm103.cuh"
 
 namespace attn {
 namespace {
