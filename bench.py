@@ -13,7 +13,8 @@ decode workload (HBM GB/s), an end-to-end pass through the public API from
 pinned host buffers, and the float64 CPU oracle on a bounded sample.
 
 Usage: python bench.py [--gpus N] [--steps K] [--warmup W] [--impl reference]
-       python bench.py --profile-case fwd|bwd|decode|varlen   (one small case for ncu)
+       python bench.py --profile-case fwd|bwd|decode|varlen|paged|norm|norm_bwd
+           (one small case for ncu)
 Under torchrun each rank runs its own replica (weak scaling) and rank 0
 prints one JSON line.
 """
@@ -699,6 +700,12 @@ def run_profile_case(args):
                 make several full waves of splits)
     varlen      the varlen workload (64 sequences U[100,4096], window (256,0),
                 softcap 50), forward then backward
+    paged       a serving step over a paged cache: the decode case's 16 caches
+                (--head-dim as there) with one new token each but the first,
+                which gets a chunk of 1024; appended, causal
+    norm / norm_bwd
+                per-head norm and rotation of the queries and keys of 16384
+                tokens, or its gradient (--head-dim keeps hq * d = 4096)
 
     `--calls` calls (a warm-up and the one to capture), then the device
     error word is checked."""
@@ -738,6 +745,30 @@ def run_profile_case(args):
         for _ in range(args.calls):
             libattn.bwd_varlen(q, k, v, o, lse, do, cu, cu, mx, mx,
                                deterministic=args.deterministic, **kw)
+    elif args.profile_case in ("norm", "norm_bwd"):
+        d = args.head_dim
+        b, s, hq = 1, 16384, HQ * D // d
+        q, k, gq, gk = (syn.device_normal((b, s, h, d), bf, 20 + i)
+                        for i, h in enumerate((hq, hq // 4, hq, hq // 4)))
+        wq, wk = (syn.device_normal((d,), bf, 24 + i) for i in range(2))
+        ph = libattn.rope_phases([10000.0 ** (-2 * j / d) for j in range(d // 2)])
+        kw = dict(phases=ph, q_weight=wq, k_weight=wk)
+        for _ in range(args.calls):
+            if args.profile_case == "norm":
+                libattn.qk_norm_rope(q, k, **kw)
+            else:
+                libattn.qk_norm_rope_bwd(q, k, gq, gk, **kw)
+    elif args.profile_case == "paged":
+        b, chunk, page, d = 16, 1024, 256, args.head_dim
+        seqlens, table, npages = syn.decode_layout(9, b, 32768, page, chunk)
+        new = [chunk] + [1] * (b - 1)
+        cu = torch.tensor([sum(new[:i]) for i in range(b + 1)], dtype=torch.int32).cuda()
+        kc = syn.device_normal((npages, page, HKV, d), bf, 5)
+        vc = syn.device_normal((npages, page, HKV, d), bf, 6)
+        q = syn.device_normal((sum(new), HQ, d), bf, 7)
+        sl, bt = torch.from_numpy(seqlens).cuda(), torch.from_numpy(table).cuda()
+        for _ in range(args.calls):
+            libattn.fwd_paged(q, kc, vc, cu, sl, block_table=bt, causal=True)
     else:
         b, sq, page, d = 16, args.decode_sq, 256, args.head_dim
         seqlens, table, npages = syn.decode_layout(9, b, 32768, page, sq)
@@ -765,13 +796,13 @@ def main():
     ap.add_argument("--no-extras", action="store_true", help="skip varlen/decode lines")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-accuracy", action="store_true", help="skip the oracle error sample")
-    ap.add_argument("--profile-case", choices=["fwd", "bwd", "decode", "varlen"],
+    ap.add_argument("--profile-case", choices=["fwd", "bwd", "decode", "varlen", "paged", "norm", "norm_bwd"],
                     help="run one small fixed case for a profiler capture and exit")
     ap.add_argument("--calls", type=int, default=2, help="calls of --profile-case")
     ap.add_argument("--deterministic", action="store_true", help="--profile-case bwd mode")
     ap.add_argument("--decode-sq", type=int, default=4, help="--profile-case decode: sq = s_new")
     ap.add_argument("--head-dim", type=int, default=128, choices=[64, 128, 256],
-                    help="--profile-case fwd/bwd: head dim (hq = 4096 / d); decode: head dim")
+                    help="--profile-case fwd/bwd: head dim (hq = 4096 / d), norm too; decode/paged: head dim")
     args = ap.parse_args()
     rank = int(os.environ.get("RANK", "0"))
     world = int(os.environ.get("WORLD_SIZE", "1"))

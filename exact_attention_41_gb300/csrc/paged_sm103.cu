@@ -6,34 +6,42 @@
 // keys with S and P in TMEM only.  What differs is where work and keys come
 // from.
 //
-// Work.  A block takes one item: a tile of query rows (one or two times 128;
-// with GQA the g heads of a KV head share a tile, 128 / g positions of each),
-// one KV head, and one piece of the tile's visible keys.  Lengths are known on
-// the device only, so every block finds its item itself: one warp runs over
-// cu_seqlens and cache_seqlens, 32 sequences at a time, counts each one's
-// tiles and pieces and stops where its block index falls.  The grid is the
-// largest number of items that the sizes on the host allow; blocks behind the
-// last item leave at once.  A batch of one long chunk among many single
-// tokens therefore costs no grid of longest-length rows.
+// Work.  A block takes one item: a tile of 128 query rows (with GQA the g heads
+// of a KV head share it, 128 / g positions of each), one head, and one piece of
+// the tile's visible keys.  Lengths are known on the device only, so every block
+// finds its item itself: its warps read all lengths into shared memory as tiles
+// and key steps, and one warp counts items, 32 sequences at a time, up to its
+// block index.  The grid is the largest number of items that the sizes on the
+// host allow; blocks behind the last item leave at once.  A batch of one long
+// chunk among many single tokens therefore costs no grid of longest-length rows.
 //
-// Pieces.  With few query rows the keys are cut so that the call fills the
-// GPU: all sequences' key steps together, divided by the wanted number of
-// items, give the length of a piece.  Pieces of a cut row write a normalised
-// fp32 O and its log2-sum; the block that writes the last piece of a tile joins
-// them, in piece order.
+// Pieces.  With few tiles the keys are cut, so that the call fills whole waves of
+// blocks: all key steps together, and what starting blocks and joining pieces
+// costs, give the steps of a piece (choose_piece).  Pieces of a cut row write a
+// normalised fp32 O and its log2-sum; the block that writes the last piece of a
+// tile joins them, in piece order, so the result is the same every run.
 //
 // Keys.  A K or V tile of BN keys is one TMA box where a page holds a multiple
 // of BN keys, and otherwise one box per gcd(page_size, BN) keys, issued by as
-// many lanes, each of which looks its page up one step ahead.  Boxes without a
-// visible key are not loaded and their table entries not read.  Slots outside
-// the block's visible keys may hold anything, and 0 * NaN would reach O, so the
-// producer warp zeroes those rows of the first and last V tile in shared
-// memory before their product is issued; in K they only reach scores that the
-// mask overwrites.
+// many lanes; a lane holds the page of one of the next 32 boxes and looks up that
+// of the 32 behind them.  Boxes without a visible key are not loaded and their
+// table entries not read.  Slots outside the block's visible keys may hold
+// anything, and 0 * NaN would reach O, so the V producer zeroes those rows of the
+// first and last V tile in shared memory before their product is issued; in K
+// they only reach scores that the mask overwrites.
 //
-// Roles as in the dense forward: warp 0 producer, warp 1 MMA issuer, one
-// softmax warpgroup per 128-row tile.  Softmax warps whose 32 rows are all
-// beyond the sequence do nothing.
+// Roles.  Warp 0 finds the item and loads Q and K, warp 6 loads V, warp 1 issues
+// the products, warps 2-5 are the softmax, one row a thread; those whose 32 rows
+// are all beyond the sequence do nothing.
+//
+// What bounds it (bf16; measured copy 6.8 TB/s, cuBLAS 1.9 PFLOP/s):
+//   64 single tokens, 32/8 heads of 128, 32K caches    7.1 TB/s, the memory
+//   24 drafts of 2-9 tokens, 16/4 heads of 64          4.9 TB/s: two waves of
+//                                                      blocks, joined pieces
+//   a chunk of 8192 behind 16K, 32/8 heads of 128      1.45 PFLOP/s: softmax and
+//                                                      products take turns
+//   chunks in a window, softcap, 8/2 heads of 256      0.5 PFLOP/s: one block a SM,
+//                                                      the exponential unit
 #include <algorithm>
 #include <numeric>
 
@@ -255,7 +263,8 @@ __device__ __forceinline__ bool find_item(const PagedArgs &a, const Shapes &sh, 
   // Order: sequences of several tiles are bound by the tensor cores, those of
   // one tile mostly by memory.  Where a call has both, their items alternate in
   // proportion, so that the two kinds of blocks run beside one another.
-  // (47 single tokens and a chunk of 2001: 285 us in sequence order, 266 so.)
+  // (47 single tokens and a chunk of 2001: 285 us in sequence order, 266 so,
+  // before the later steps.)
   bool mixed = sh.long_pairs > 0.f && sh.long_pairs < sh.pairs, is_long = false;
   if (mixed) {
     uint32_t n_long = 0, n_all = 0;
