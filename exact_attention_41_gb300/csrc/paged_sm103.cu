@@ -34,14 +34,18 @@
 // the products, warps 2-5 are the softmax, one row a thread; those whose 32 rows
 // are all beyond the sequence do nothing.
 //
-// What bounds it (bf16; measured copy 6.8 TB/s, cuBLAS 1.9 PFLOP/s):
-//   64 single tokens, 32/8 heads of 128, 32K caches    7.1 TB/s, the memory
-//   24 drafts of 2-9 tokens, 16/4 heads of 64          4.9 TB/s: two waves of
-//                                                      blocks, joined pieces
-//   a chunk of 8192 behind 16K, 32/8 heads of 128      1.45 PFLOP/s: softmax and
-//                                                      products take turns
-//   chunks in a window, softcap, 8/2 heads of 256      0.5 PFLOP/s: one block a SM,
-//                                                      the exponential unit
+// What bounds it (measured copy 6.8 TB/s, cuBLAS bf16 1.9 PFLOP/s):
+//   64 single tokens, caches up to 32K, 32/8 heads of 128: 7.1 TB/s; the memory.
+//   24 drafts of 2-9 tokens, 64/8 heads of 64: 4.9 TB/s; blocks' starts and the
+//     joining of pieces, in two waves.
+//   a chunk of 8192 behind 24K, 32/8 heads of 128: 1.46 PFLOP/s; products and
+//     softmax of two blocks a SM, as in the dense forward.
+//   47 single tokens and a chunk of 2001: 3.5 TB/s and 0.81 PFLOP/s at once; a
+//     chunk's block beside a token's has the tensor cores to itself and waits for
+//     its own softmax.
+//   12 chunks of 100-1000 in a window of 1024, 8/4 heads of 256: 0.5 PFLOP/s; one
+//     block a SM, whose start (5 us) and end (4 us) nothing covers.  Long chunks
+//     there run at 1.25 PFLOP/s.
 #include <algorithm>
 #include <numeric>
 

@@ -21,6 +21,13 @@
 // cosines and sines are then the same for every head of the token, and a head
 // is D / 16 neighbouring lanes, so the norm's sum is log2(D / 16) shuffles.
 // Everything is held in fp32 and rounded once, to the output.
+//
+// Bound by memory: each element is read once and written once (the gradient reads
+// two and writes one).  32768 tokens, 32/8 heads of 128, bf16: 106 us forward
+// (6.3 TB/s of a measured copy's 6.8), 156 us backward (6.5 TB/s).  14239 tokens
+// into 16-token pages, 32/8 heads of 64: 34.5 us (5.1 TB/s; 26 at the copy's
+// rate).  64 tokens: 3.6 us, of which a launch and three trips to memory, one
+// after another (offsets, page, head), are nearly all.
 #include <algorithm>
 
 #include "copies.cuh"

@@ -105,18 +105,20 @@ def _check(status: int, what: str):
 
 
 _torch_module = None
-_raw_stream = None
+_raw_stream = _device = None  # the current device's stream handle; the current device
 
 
 def _torch():
     """torch, imported at the first use (host-only calls do without it)."""
-    global _torch_module, _raw_stream
+    global _torch_module, _raw_stream, _device
     if _torch_module is None:
         import torch
 
         _torch_module = torch
         # (the stream's handle without a Stream object around it: 3 us less a call)
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        # (once a CUDA tensor is there, without the check that CUDA is set up)
+        _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     return _torch_module
 
 
@@ -456,11 +458,10 @@ def _call(fn, args, dense, strided=()):
             i = t.get_device()
             if i != index:
                 index = _same_device(index, i)
-    cuda = _torch_module.cuda
-    if index == cuda.current_device():
-        st = fn(*args, _stream())
+    if index == _device():
+        st = fn(*args, _raw_stream(index) if _raw_stream else _stream())
     else:
-        with cuda.device(index):
+        with _torch_module.cuda.device(index):
             st = fn(*args, _stream())
     if st != 0:
         raise AttnError(st, fn.__name__)

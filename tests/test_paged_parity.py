@@ -171,7 +171,7 @@ def test_many_sequences():
 
 @pytest.mark.parametrize("d", [64, 128])
 def test_long_chunk_with_few_pages_seen(d):
-    """A chunk of 1500 rows (two tiles a block) behind 1000 tokens; then the same
+    """A chunk of 1500 rows behind 1000 tokens; then the same
     under a window, with the pages before it gone."""
     c = make(6, [1500], [1000], 8, 2, d, 64, syn.BF16)
     run(c, causal=True)
@@ -283,7 +283,7 @@ def test_offsets_out_of_order_or_past_the_rows():
 
 @pytest.mark.parametrize("d,new", [(64, 40), (128, 40), (128, 1500), (256, 40)])
 def test_wait_timeout_is_reported_and_recoverable(d, new):
-    """Every layout: the MMA issuer's first wait can only run out; the call is
+    """Every head dim: the MMA issuer's first wait can only run out; the call is
     abandoned with the timeout bit, and the next one is right."""
     import torch
 
