@@ -596,7 +596,6 @@ attn_status attn_fwd_paged(const void *q, const void *k_cache, const void *v_cac
   a.slots = (int)plan.slots;
   a.o_part = static_cast<float *>(workspace);
   a.lse_part = a.o_part + plan.slots * 128 * d;
-  a.written = reinterpret_cast<int *>(a.lse_part + plan.slots * 128);
   if (num_pages == 0 || (block_table && page_size % 16 != 0))
     return launched(launch_paged_simt(a, stream));
   return launched(launch_paged_tc(a, plan, stream));

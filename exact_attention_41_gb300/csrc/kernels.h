@@ -97,7 +97,6 @@ struct PagedArgs {
   int num_splits, wave, max_waves, slots;
   float *o_part;                // (slots, 128, d)
   float *lse_part;              // (slots, 128), log2 units
-  int *written;                 // (slots) pieces written, at a pair's first slot
 };
 
 // How attn_fwd_paged cuts its work; host only, from the sizes of the call.

@@ -48,6 +48,7 @@
 //     there run at 1.25 PFLOP/s.
 #include <algorithm>
 #include <numeric>
+#include <type_traits>
 
 #include "copies.cuh"
 #include "paged.cuh"
@@ -59,9 +60,7 @@ using namespace sm103;
 constexpr int kBM = 128;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O when max grows > 256x
 constexpr int kMaxStages = 5;
-constexpr int kMaxWarps = 7;
-constexpr int kJoinRing = 8;        // tiles of 8 KB
-constexpr int kJoinWeights = 8192;  // rows x pieces
+constexpr int kMaxWarps = 6;
 constexpr int kMinPieceSteps = 4;          // shortest piece worth a block and a partial result
 constexpr int kBlockSteps = 8;             // a block's start and end, in steps
 // what joining adds to a call, in steps: a step per so many values of a piece,
@@ -86,13 +85,9 @@ struct PagedCfg {
   static constexpr int kSmem = kSmemData + 1024;
   static constexpr int kSCol0 = D;
   static constexpr uint32_t kTmemCols = kCtas == 2 ? 256 : 512;
-  // warp 0: K producer, 1: MMA issuer, 2-5: softmax, 6: V producer
-  static constexpr int kThreads = 224;
+  // warp 0: producer, 1: MMA issuer, 2-5: softmax
+  static constexpr int kThreads = 192;
   static constexpr int kSoftmaxWarp0 = 2;
-  static constexpr int kSoftmaxWarps = 4;
-  static constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
-  static constexpr int kVWarp = 6;
-  static_assert(kJoinRing * 8192 + kJoinWeights * 4 <= kSmemData, "room for join_bulk");
   static_assert(D + 2 * BN <= (int)kTmemCols, "TMEM budget");
   static_assert(kCtas == 1 || 2 * (kSmem + 2048) <= 227 * 1024, "shared memory of two blocks");
 };
@@ -172,6 +167,14 @@ __device__ __forceinline__ Shapes gather_shapes(const PagedArgs &a, Shape *at, i
   }
   return Shapes{at, warp_sum(work), warp_sum(pairs), warp_sum(long_pairs),
                 __reduce_max_sync(0xffffffffu, longest), __reduce_max_sync(0xffffffffu, rows)};
+}
+
+__device__ __forceinline__ void add_shapes(Shapes &to, const Shapes &s) {
+  to.work += s.work;
+  to.pairs += s.pairs;
+  to.long_pairs += s.long_pairs;
+  to.longest = max(to.longest, s.longest);
+  to.rows = max(to.rows, s.rows);
 }
 
 // x / y for x < 2^24 or so, y > 0 alike in the whole grid: a reciprocal and a
@@ -375,14 +378,14 @@ struct Shared {
   uint64_t s_full[2], p_full[2], o_done;
   uint64_t v_clean[2];  // first / last V tile: rows that no query sees are zeroed
   uint64_t all_done;    // every MMA of the block has completed
-  uint64_t joined[2];   // groups of pieces have landed
   uint64_t wait_ns;
   Item item;
   Piece piece;
   Shapes sums[kMaxWarps];  // of the warps' sequences
   uint32_t tmem_base;
   int abort;
-  int joins;               // this block joins the pair's pieces
+  int issued;              // K and V tiles whose copies have been issued (2 j: K of step j)
+  Box box[32];             // boxes of the next steps
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -401,29 +404,25 @@ __device__ __forceinline__ bool wait_warp(Shared &sh, uint64_t *bar, uint32_t pa
 template <typename T> struct IsBf16 { static constexpr int v = 0; };
 template <> struct IsBf16<__nv_bfloat16> { static constexpr int v = 1; };
 
-// Joins the n pieces of a pair: with l_p the log2-sums, L = log2 sum 2^l_p and
-// O = sum 2^(l_p - L) O_p, in key order, so the result does not depend on who
-// finishes last.  Called by the kWarps softmax warps, once per block at most and
-// with few instructions between them, so what counts is the number of trips to
-// L2 one after another: a warp takes kR rows at a time, a lane four columns (and
-// for d = 256 four more), asks for the sums and the first kP pieces at once, and
-// has the weights ready in its lanes when the pieces arrive.  (Read past L1:
-// other blocks have written them.)
+// Joins the n pieces of rows [x_lo, rows) of a pair: with l_p the log2-sums, L = log2
+// sum 2^l_p and O = sum 2^(l_p - L) O_p, in key order.  What counts is the number of
+// trips to L2 one after another: a warp takes kR rows at a time, a lane four columns
+// (and for d = 256 four more), asks for the sums and the first kP pieces at once, and
+// has the weights ready in its lanes when the pieces arrive.
 template <typename T, int D, int kWarps, int kR, int kP>
 __device__ __forceinline__ void join_rows(const PagedArgs &a, const Item &it, int n, int slot0,
-                                          int tile_pos, int warp) {
+                                          int x_lo, int rows, int warp) {
   constexpr int LPR = D / 4 < 32 ? D / 4 : 32;  // lanes of a row
   constexpr int QP = D / 4 / LPR;               // column quads of a lane
   constexpr int RPW = 32 / LPR;                 // rows side by side in a warp
   const int lane = threadIdx.x & 31, sub = lane % LPR, pg = a.pack;
-  const int rows = min(it.s.lq - it.m0, tile_pos) * pg;
   const uint32_t inv_pg = (65536 + pg - 1) / pg;  // x / pg = x inv_pg >> 16 for x < 256
   const int64_t step = (int64_t)it.stride * kBM;  // rows from a piece to the next
   const float *l_at = a.lse_part + (int64_t)slot0 * kBM;
   const float4 *o_at = reinterpret_cast<const float4 *>(a.o_part) +
                        (int64_t)slot0 * kBM * (D / 4) + sub;
   constexpr int kStep = kWarps * RPW;  // rows from one of a warp's to its next
-  for (int x0 = warp * RPW; x0 < rows; x0 += kR * kStep) {
+  for (int x0 = x_lo + warp * RPW; x0 < rows; x0 += kR * kStep) {
     const int xl = x0 + lane / LPR;
     int64_t at[kR];  // of the row in its slot
     float l[kR], w[kR], lse[kR];
@@ -497,104 +496,6 @@ __device__ __forceinline__ void join_rows(const PagedArgs &a, const Item &it, in
   }
 }
 
-// The same for tiles of many rows, where bytes in flight count (join_rows: 8
-// bytes a cycle).  RB rows of a piece lie together in the workspace, 8 KB, and
-// come as one bulk copy; up to kGroup pieces of the same rows make a group, which
-// is waited for and handed back as one (a wait per copy: 11 bytes a cycle), and
-// two groups are in flight or in use.  The weights of all rows and pieces go to
-// shared memory first.  Called by the kThreads softmax threads.
-template <typename T, int D, int kThreads>
-__device__ __forceinline__ void join_bulk(const PagedArgs &a, const Item &it, int n, int slot0,
-                                          int tile_pos, int tid, uint64_t *full, uint8_t *ring) {
-  constexpr int RB = 2048 / D, kTile = RB * D * 4, kQuads = RB * D / 4 / kThreads;
-  constexpr int kGroup = kJoinRing / 2;
-  static_assert(RB * D / 4 % kThreads == 0, "whole quads");
-  float *w = reinterpret_cast<float *>(ring + kJoinRing * kTile);
-  const int pg = a.pack, rows = min(it.s.lq - it.m0, tile_pos) * pg;
-  const uint32_t inv_pg = (65536 + pg - 1) / pg;  // x / pg = x inv_pg >> 16 for x < 256
-  const int64_t step = (int64_t)it.stride * kBM;  // rows from a piece to the next
-  const int batches = (rows + RB - 1) / RB, parts = (n + kGroup - 1) / kGroup;
-  const float *o_at = a.o_part + (int64_t)slot0 * kBM * D;
-  const auto issue = [&](int i) {  // group i; one thread
-    const int b = i / parts, p0 = (i - b * parts) * kGroup, some = min(kGroup, n - p0);
-    const uint32_t bytes = min(RB, rows - b * RB) * D * 4;
-    mbar_expect_tx(&full[i & 1], bytes * some);
-    for (int p = 0; p < some; ++p)
-      bulk_load(ring + ((i & 1) * kGroup + p) * kTile,
-                o_at + ((int64_t)b * RB + (p0 + p) * step) * D, bytes, &full[i & 1]);
-  };
-  if (tid == 0) {
-    fence_async();
-    issue(0);
-    if (batches * parts > 1) issue(1);
-  }
-  for (int x = tid; x < rows; x += kThreads) {
-    const float *l = a.lse_part + (int64_t)slot0 * kBM + x;
-    float m = -INFINITY, sum = 0.f;
-#pragma unroll 4
-    for (int p = 0; p < n; ++p) {
-      const float v = __ldcg(l + p * step);
-      w[x * n + p] = v;
-      m = fmaxf(m, v);
-    }
-    const float ref = m > -INFINITY ? m : 0.f;
-    for (int p = 0; p < n; ++p) {
-      const float e = exp2f(w[x * n + p] - ref);
-      w[x * n + p] = e;
-      sum += e;
-    }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    for (int p = 0; p < n; ++p) w[x * n + p] *= inv;
-    const int p = (int)(x * inv_pg >> 16);
-    const int hr = pg > 1 ? it.head * pg + x - p * pg : it.head;
-    a.lse[(int64_t)hr * a.total_q + it.s.q0 + it.m0 + p] =
-        sum > 0.f ? (ref + log2f(sum)) * kLn2 : -INFINITY;
-  }
-  named_bar_sync(1, kThreads);
-  int i = 0;
-  for (int b = 0; b < batches; ++b) {
-    float o[kQuads][4] = {};
-    const float *wr[kQuads];
-#pragma unroll
-    for (int k = 0; k < kQuads; ++k)
-      wr[k] = w + min(b * RB + (tid + k * kThreads) / (D / 4), rows - 1) * n;
-    for (int p0 = 0; p0 < n; p0 += kGroup, ++i) {
-      // (a copy that never lands raises the error word; all threads go on alike)
-      mbar_wait(&full[i & 1], (i >> 1) & 1, a.err);
-      const float4 *src = reinterpret_cast<const float4 *>(ring + (i & 1) * kGroup * kTile) + tid;
-#pragma unroll
-      for (int p = 0; p < kGroup; ++p) {
-        if (p0 + p < n) {
-#pragma unroll
-          for (int k = 0; k < kQuads; ++k) {
-            const float4 v = src[p * (kTile / 16) + k * kThreads];
-            const float wp = wr[k][p0 + p];
-            o[k][0] = fmaf(wp, v.x, o[k][0]);
-            o[k][1] = fmaf(wp, v.y, o[k][1]);
-            o[k][2] = fmaf(wp, v.z, o[k][2]);
-            o[k][3] = fmaf(wp, v.w, o[k][3]);
-          }
-        }
-      }
-      named_bar_sync(1, kThreads);
-      if (tid == 0 && i + 2 < batches * parts) {
-        fence_async();
-        issue(i + 2);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kQuads; ++k) {
-      const int y = tid + k * kThreads, x = b * RB + y / (D / 4);
-      if (x < rows) {
-        const int p = (int)(x * inv_pg >> 16);
-        const int hr = pg > 1 ? it.head * pg + x - p * pg : it.head;
-        const int64_t row = it.s.q0 + it.m0 + p;
-        store_vec<T, 4>(static_cast<T *>(a.o) + (row * a.hq + hr) * D + y % (D / 4) * 4, o[k]);
-      }
-    }
-  }
-}
-
 template <typename T, int D, int BN>
 __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kCtas)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -612,52 +513,17 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pg = a.pack;
-  // shapes of the sequences: every warp but the one that allocates TMEM
   Shapes shapes{reinterpret_cast<Shape *>(smem), 0.f, 0.f, 0.f, 0, 0};
-  constexpr int kGather = C::kThreads / 32 - 1;
-  if (warp == 1) {
-    tmem_alloc(&sh.tmem_base, C::kTmemCols);
-    tmem_relinquish();
-  } else {
-    if (threadIdx.x == C::kVWarp * 32) {
-      prefetch_tmap(&tq);
-      prefetch_tmap(&tk);
-      prefetch_tmap(&tv);
-      mbar_init(&sh.q_full, 1);
-      for (int s = 0; s < ST; ++s) {
-        mbar_init(&sh.k_full[s], 1);
-        mbar_init(&sh.k_empty[s], 1);
-        mbar_init(&sh.v_full[s], 1);
-        mbar_init(&sh.v_empty[s], 1);
-      }
-      for (int s = 0; s < 2; ++s) {
-        mbar_init(&sh.s_full[s], 1);
-        mbar_init(&sh.v_clean[s], 1);
-      }
-      mbar_init(&sh.o_done, 1);
-      mbar_init(&sh.all_done, 1);
-      for (int s = 0; s < 2; ++s) mbar_init(&sh.joined[s], 1);
-      sh.wait_ns = a.wait_ns;
-      sh.abort = 0;
-      fence_mbar_init();
-    }
-    const int w = warp == 0 ? 0 : warp - 1;
-    if (w * 32 < a.batch) {
-      const Shapes sum = gather_shapes(a, shapes.at, w, kGather, tile_pos, BN, blockIdx.x == 0);
-      if (lane == 0) sh.sums[w] = sum;
-    }
+  constexpr int kGather = C::kThreads / 32;
+  if (warp * 32 < a.batch) {
+    const Shapes sum = gather_shapes(a, shapes.at, warp, kGather, tile_pos, BN, blockIdx.x == 0);
+    if (lane == 0) sh.sums[warp] = sum;
   }
   if (a.batch > 32) __syncthreads();  // (else warp 0 has gathered all)
-  Box early{-1, 0};  // the K producer's first boxes, on their way before the others start
+  Box early{-1, 0};  // the producer's first boxes, on their way before the others start
   if (warp == 0) {
     __syncwarp();
-    for (int w = 0; w < kGather && w * 32 < a.batch; ++w) {
-      shapes.work += sh.sums[w].work;
-      shapes.pairs += sh.sums[w].pairs;
-      shapes.long_pairs += sh.sums[w].long_pairs;
-      shapes.longest = max(shapes.longest, sh.sums[w].longest);
-      shapes.rows = max(shapes.rows, sh.sums[w].rows);
-    }
+    for (int w = 0; w < kGather && w * 32 < a.batch; ++w) add_shapes(shapes, sh.sums[w]);
     Item it{};
     it.pieces = 1;
     const bool found = find_item(a, shapes, blockIdx.x, tile_pos, BN, it);
@@ -666,44 +532,97 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
     if (lane == 0) {
       sh.item = it;
       sh.piece = p;
-      // softmax threads that take part: warps with a row of the sequence
-      const int rows = min(max(it.s.lq - it.m0, 0), tile_pos) * pg;
-      for (int s = 0; s < 2; ++s) mbar_init(&sh.p_full[s], max(1, (rows + 31) / 32 * 32));
-      fence_mbar_init();
     }
   }
   // (the shapes were where Q lands next)
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncthreads();
+  const Item it = sh.item;
+  const Piece pc = sh.piece;
+  if (!pc.live) return;  // no work
+  if (threadIdx.x == C::kSoftmaxWarp0 * 32) {
+    mbar_init(&sh.q_full, 1);
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&sh.k_full[s], 1);
+      mbar_init(&sh.k_empty[s], 1);
+      mbar_init(&sh.v_full[s], 1);
+      mbar_init(&sh.v_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sh.s_full[s], 1);
+      mbar_init(&sh.p_full[s], kBM);
+      mbar_init(&sh.v_clean[s], 1);
+    }
+    mbar_init(&sh.o_done, 1);
+    mbar_init(&sh.all_done, 1);
+    sh.wait_ns = a.wait_ns;
+    sh.abort = 0;
+    sh.issued = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sh.tmem_base, C::kTmemCols);
+    tmem_relinquish();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
-  const Item it = sh.item;
-  const Piece pc = sh.piece;
   const PagedSeq sq = it.s;
   const int kvh = pg > 1 ? it.head : it.head / (a.hq / a.hkv);
   const int h = pg > 1 ? kvh * pg : it.head;  // (first) query head of the rows
   const int n_lo = pc.n_lo, nt = pc.nt, front = pc.front, back = pc.back;
-  const bool live = pc.live;
-  if (warp < C::kSoftmaxWarp0 || warp >= C::kSoftmaxWarp0 + C::kSoftmaxWarps) {
-    if (warp == 0 || warp == C::kVWarp) {
-      // ----------------------------------------- producers: warp 0 K, kVWarp V
+  if (warp < C::kSoftmaxWarp0) {
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      // All lanes look pages up; one thread issues the copies, in stretches behind
+      // which the lanes meet.
       if (nt > 0) {
-        const bool is_v = warp != 0;
-        const CUtensorMap *map = is_v ? &tv : &tk;
-        uint64_t *full = is_v ? sh.v_full : sh.k_full, *empty = is_v ? sh.v_empty : sh.k_empty;
-        const int boxes = BN / box_rows;  // a power of two
-        const int box = lane / C::kCols, col = lane % C::kCols;  // this lane's part of a tile
+        const int boxes = BN / box_rows, per = 32 / boxes;  // powers of two
         const int key_lo = n_lo * BN;
-        uint8_t *dst = (is_v ? v_s : k_s) + col * (BN * 128) + box * box_rows * 128;
-        Box now{-1, 0}, ahead = is_v ? fetch_boxes(a, it, pc, boxes, box_rows, key_lo, 0) : early;
-        if (!is_v && lane == 0) {
+        Box ahead = early;
+        if (elect_one()) {
           mbar_expect_tx(&sh.q_full, tile_pos * pg * D * 2);
           for (int c = 0; c < C::kCols; ++c)
             tma_load_3d(q_s + c * kBM * 128, &tq, &sh.q_full, c * 64, h, sq.q0 + it.m0);
         }
+        __syncwarp();
+        // copies of the steps [j0, j1)
+        const auto issue = [&](int j0, int j1) {
+          if (elect_one()) {
+            for (int j = j0; j < j1; ++j) {
+              const int st = j % ST;
+              const uint32_t ph = (j / ST) & 1;
+              const Box *bx = &sh.box[j % per * boxes];
+              int n = 0;
+              for (int b = 0; b < boxes; ++b) n += bx[b].page >= 0;
+              const uint32_t bytes = n * box_rows * D * 2;
+              if (!wait_bar(sh, &sh.k_empty[st], ph ^ 1, a.err)) break;
+              mbar_expect_tx(&sh.k_full[st], bytes);
+              for (int b = 0; b < boxes; ++b) {
+                const Box x = bx[b];
+                if (x.page < 0) continue;
+                for (int c = 0; c < C::kCols; ++c)
+                  tma_load_4d(k_s + st * C::kKVBytes + c * (BN * 128) + b * box_rows * 128, &tk,
+                              &sh.k_full[st], c * 64, kvh, x.slot, x.page);
+              }
+              sh.issued = 2 * j + 1;
+              if (!wait_bar(sh, &sh.v_empty[st], ph ^ 1, a.err)) break;
+              mbar_expect_tx(&sh.v_full[st], bytes);
+              for (int b = 0; b < boxes; ++b) {
+                const Box x = bx[b];
+                if (x.page < 0) continue;
+                for (int c = 0; c < C::kCols; ++c)
+                  tma_load_4d(v_s + st * C::kKVBytes + c * (BN * 128) + b * box_rows * 128, &tv,
+                              &sh.v_full[st], c * 64, kvh, x.slot, x.page);
+              }
+              sh.issued = 2 * j + 2;
+            }
+          }
+          __syncwarp();
+        };
         // zeroes rows [r0, r1) of V tile j once it has landed
-        auto clean = [&](int j, int r0, int r1, uint64_t *bar) {
+        const auto clean = [&](int j, int r0, int r1, uint64_t *bar) {
           if (!wait_warp(sh, &sh.v_full[j % ST], (j / ST) & 1, a.err)) return;
           uint8_t *tile = v_s + (j % ST) * C::kKVBytes;
           for (int x = lane; x < (r1 - r0) * C::kCols * 8; x += 32) {
@@ -714,51 +633,45 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) mbar_arrive(bar);
+          __syncwarp();
         };
-        const int front_after = min(ST, nt) - 1;  // step after whose load the first tile is cleaned
-        int issued = 0;
-        for (int j = 0; j < nt; ++j) {
-          const int st = j % ST;
-          const int in32 = j * boxes % 32;
-          if (in32 == 0) {
-            now = ahead;
-            if (__any_sync(0xffffffffu, now.page == -2)) {
-              if (lane == 0) {
-                raise_error(a.err, kErrPageOutOfRange);
-                *(volatile int *)&sh.abort = 1;
-              }
-              break;
+        for (int j0 = 0; j0 < nt; j0 += per) {
+          if (__any_sync(0xffffffffu, ahead.page == -2)) {
+            if (lane == 0) {
+              raise_error(a.err, kErrPageOutOfRange);
+              *(volatile int *)&sh.abort = 1;
             }
-            ahead = fetch_boxes(a, it, pc, boxes, box_rows, key_lo, j * boxes + 32);
+            __syncwarp();
+            break;
           }
-          const int page = __shfl_sync(0xffffffffu, now.page, (in32 + box) & 31);
-          const int slot = __shfl_sync(0xffffffffu, now.slot, (in32 + box) & 31);
-          const bool load = box < boxes && page >= 0;
-          const uint32_t bytes =
-              (uint32_t)__popc(__ballot_sync(0xffffffffu, load)) * box_rows * 128;
-          bool ok = true;
-          if (lane == 0) {
-            ok = wait_bar(sh, &empty[st], ((j / ST) & 1) ^ 1, a.err);
-            if (ok) mbar_expect_tx(&full[st], bytes);
+          sh.box[lane] = ahead;
+          ahead = fetch_boxes(a, it, pc, boxes, box_rows, key_lo, (j0 + per) * boxes);
+          __syncwarp();
+          const int j1 = min(nt, j0 + per);
+          int j = j0;
+          if (j0 == 0 && front > 0) {  // the first V tile, once as many as fit are on their way
+            j = min(ST, nt);
+            issue(0, j);
+            clean(0, 0, min(front, BN), &sh.v_clean[0]);
           }
-          if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-          if (load) tma_load_4d(dst + st * C::kKVBytes, map, &full[st], col * 64, kvh, slot, page);
-          issued = j + 1;
-          if (is_v && j == front_after && front > 0) clean(0, 0, min(front, BN), &sh.v_clean[0]);
+          issue(j, j1);
+          if (__any_sync(0xffffffffu, *(volatile int *)&sh.abort)) break;
         }
-        if (is_v && issued == nt && back > 0) clean(nt - 1, BN - back, BN, &sh.v_clean[1]);
-        __syncwarp();
+        const int issued = *(volatile int *)&sh.issued;
+        if (issued == 2 * nt && back > 0) clean(nt - 1, BN - back, BN, &sh.v_clean[1]);
         if (*(volatile int *)&sh.abort) {
-          // let this warp's copies in flight land before the block exits
+          // let the copies in flight land before the block exits
           int *noerr = nullptr;
-          if (!is_v) mbar_wait(&sh.q_full, 0, noerr);
-          for (int j = max(0, issued - ST); j < issued; ++j)
-            mbar_wait(&full[j % ST], (j / ST) & 1, noerr);
+          mbar_wait(&sh.q_full, 0, noerr);
+          for (int x = max(0, issued - 2 * ST); x < issued; ++x) {
+            const int j = x / 2, st = j % ST;
+            mbar_wait(x % 2 ? &sh.v_full[st] : &sh.k_full[st], (j / ST) & 1, noerr);
+          }
         }
       }
-    } else if (warp == 1) {
+    } else {
       // -------------------------------------------------------- MMA issuer
-      if (elect_one() && live) {
+      if (elect_one()) {
         constexpr int ab = IsBf16<T>::v;
         constexpr uint32_t id_s = idesc_f16(kBM, BN, ab, 0, 0);
         constexpr uint32_t id_o = idesc_f16(kBM, D, ab, 0, 1);
@@ -827,14 +740,14 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
     const int r0 = 32 * (warp & 3), r = r0 + lane;  // TMEM lane = row in the tile
     const int first = it.m0;                        // the tile's first query position
     const int rows = min(max(sq.lq - first, 0), tile_pos) * pg;  // its rows in the sequence
-    if (live && r0 < rows) {
+    {
       const int i = first + r / pg;  // query position
       const int hr = h + r % pg;     // and query head
       const uint32_t lane_off = (uint32_t)r0 << 16;
       const uint32_t o_t = tmem + lane_off;
       int lo_i, hi_i;
       key_range(i, sq.lq, sq.lk, a.win_l, a.win_r, lo_i, hi_i);
-      const uint32_t n_vis = (uint32_t)max(hi_i - lo_i + 1, 0);  // keys this row sees
+      const uint32_t n_vis = r < rows ? (uint32_t)max(hi_i - lo_i + 1, 0) : 0u;  // keys this row sees
       // steps that need no mask: every row of the tile sees every key of them
       int lo_tile_max, hi_tile_min, dummy;
       key_range(min(first + tile_pos, sq.lq) - 1, sq.lq, sq.lk, a.win_l, a.win_r, lo_tile_max, dummy);
@@ -982,6 +895,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
       const int64_t part = (int64_t)it.slot * kBM + r;
 #pragma unroll 1
       for (int c2 = 0; c2 < D / 64; ++c2) {
+        __syncwarp();  // (lanes without a row stored nothing)
         uint32_t u[64];
         if (ok && nt > 0) {
           tmem_ld32(o_t + c2 * 64, *reinterpret_cast<uint32_t(*)[32]>(u));
@@ -1017,52 +931,53 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
         else if (it.slot < a.slots)
           a.lse_part[part] = lse2;
       }
-      if (it.pieces > 1) __threadfence();  // before the piece is counted as written
-    }
-    // The block that writes the last piece of a pair joins them (its softmax
-    // warps, which have the registers for it; every copy and product of the
-    // block has completed, so the tiles' space is free).
-    // (the item is read again from shared memory: registers are short above)
-    if (live && reinterpret_cast<volatile int &>(sh.item.pieces) > 1) {
-      named_bar_sync(1, C::kSoftmaxThreads);
-      const Item jt = sh.item;
-      const int n = sh.piece.written;
-      const int slot0 = jt.slot - jt.piece * jt.stride;  // of the first piece
-      const int tid = threadIdx.x - 32 * C::kSoftmaxWarp0;
-      const bool fits = slot0 + (n - 1) * jt.stride < a.slots;
-      if (tid == 0) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");  // paged_zero_kernel, long done
-        sh.joins = fits && atomicAdd(&a.written[slot0], 1) == n - 1;
-        __threadfence();
-      }
-      named_bar_sync(1, C::kSoftmaxThreads);
-      if (sh.joins) {
-        // Few rows (single tokens): a warp per row, many pieces at a time.  Many:
-        // through shared memory, if the weights fit beside the ring, and if no
-        // copy of an abandoned piece may still be landing there.
-        const int rows = min(jt.s.lq - jt.m0, tile_pos) * a.pack;
-        if (rows <= 4 * C::kSoftmaxWarps)
-          join_rows<T, D, C::kSoftmaxWarps, 1, 4>(a, jt, n, slot0, tile_pos, tid >> 5);
-        else if (rows * n <= kJoinWeights && !*(volatile int *)&sh.abort)
-          join_bulk<T, D, C::kSoftmaxThreads>(a, jt, n, slot0, tile_pos, tid, sh.joined, smem);
-        else
-          join_rows<T, D, C::kSoftmaxWarps, 2, 4>(a, jt, n, slot0, tile_pos, tid >> 5);
-      }
     }
   }
-  // this grid, and with it the call, does not end before paged_zero_kernel
-  if (blockIdx.x == 0 && threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // The lanes of roles that one thread runs come back together here: a whole warp
+  // has to give the TMEM back.
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
+  __syncwarp();
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-// Clears the counts of written pieces.  The main kernel starts beside it (its
-// blocks wait for this grid only where they are about to hand out work), which
-// costs a call 1 us; a memset before it cost 3.
-__global__ void paged_zero_kernel(int *written, int n) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  for (int i = threadIdx.x; i < n; i += blockDim.x) written[i] = 0;
+// Joins the pieces of cut rows.  Blocks are the main kernel's: each of a pair's
+// pieces joins a share of the pair's rows.
+template <typename T, int D, int BN>
+__global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a, const int tile_pos) {
+  __shared__ Shape at[kMaxShapes];
+  __shared__ Shapes sums[4];
+  __shared__ Item item;
+  __shared__ int written;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp * 32 < a.batch) {
+    const Shapes sum = gather_shapes(a, at, warp, 4, tile_pos, BN, false);
+    if (lane == 0) sums[warp] = sum;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    Shapes all{at, 0.f, 0.f, 0.f, 0, 0};
+    for (int w = 0; w < 4 && w * 32 < a.batch; ++w) add_shapes(all, sums[w]);
+    Item it{};
+    it.pieces = 1;
+    const bool found = find_item(a, all, blockIdx.x, tile_pos, BN, it);
+    const Piece p = piece_of(a, it, tile_pos, BN, found);
+    if (lane == 0) {
+      item = it;
+      written = p.live && it.pieces > 1 ? p.written : 0;
+    }
+  }
+  __syncthreads();
+  const Item it = item;
+  const int n = written, slot0 = it.slot - it.piece * it.stride;
+  if (n == 0 || slot0 + (n - 1) * it.stride >= a.slots) return;
+  const int rows = min(it.s.lq - it.m0, tile_pos) * a.pack;
+  const int lo = rows * it.piece / n, hi = rows * (it.piece + 1) / n;
+  if (hi - lo <= 4)
+    join_rows<T, D, 4, 1, 4>(a, it, n, slot0, lo, hi, warp);
+  else
+    join_rows<T, D, 4, 2, 4>(a, it, n, slot0, lo, hi, warp);
 }
 
 // (page, slot, head, D) pool, box {64, 1, box_rows, 1}, 128-byte swizzle.
@@ -1104,18 +1019,13 @@ cudaError_t paged(const PagedArgs &a, const PagedPlan &plan, cudaStream_t st) {
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  if (plan.slots > 0) {
-    paged_zero_kernel<<<1, 1024, 0, st>>>(a.written, (int)plan.slots);
-    count_launches(1);
-    cfg.numAttrs = 1;
-  }
   e = cudaLaunchKernelEx(&cfg, paged_tc_kernel<T, D, BN>, tq, tk, tv, a, plan.tile_pos, box_rows);
   if (e != cudaSuccess) return e;
   count_launches(1);
+  if (plan.slots > 0) {
+    paged_join_kernel<T, D, BN><<<(unsigned)plan.items, 128, 0, st>>>(a, plan.tile_pos);
+    count_launches(1);
+  }
   return cudaGetLastError();
 }
 
@@ -1161,8 +1071,7 @@ PagedPlan paged_plan(int batch, int total_q, int hq, int hkv, int d, int num_spl
     p.items = p.tiles * p.num_splits;
     p.slots = p.num_splits > 1 ? p.items : 0;
   }
-  // partial O and log2-sums, and a count of written pieces per slot
-  p.ws_bytes = (size_t)p.slots * (kBM * (d + 1) * sizeof(float) + sizeof(int));
+  p.ws_bytes = (size_t)p.slots * kBM * (d + 1) * sizeof(float);  // partial O and log2-sums
   return p;
 }
 

@@ -36,7 +36,7 @@
 namespace attn {
 namespace {
 
-constexpr int kWarps = 4;       // warps of a forward or append block
+constexpr int kWarps = 2;       // warps of a forward or append block (4: 1% slower, 8: 3 to 5%)
 constexpr int kBwdWarps = 8;    // warps of a backward block
 constexpr int kBwdBlocks = 2;   // its blocks on one SM
 constexpr int kBwdStages = 4;   // heads in flight per thread: 3 ahead of the one in hand
