@@ -139,10 +139,11 @@ __device__ __forceinline__ Shape shape_of(const PagedArgs &a, const PagedSeq &s,
 
 // The shapes of all sequences, in shared memory for the first kMaxShapes (the
 // tiles' own space, which no copy uses yet), and sums over all of them.
-constexpr int kMaxShapes = 4096;
+constexpr int kMaxShapes = 4096, kJoinShapes = 1024;
 constexpr int kMaxSplits = 1024;
 struct Shapes {
   Shape *at;
+  int cap;            // sequences that `at` holds
   float work, pairs;  // per head: key steps; tiles
   float long_pairs;   // those of sequences of several tiles
   int longest;        // steps
@@ -150,7 +151,7 @@ struct Shapes {
 };
 // One warp's share, sequences `warp` * 32 + lane and on by `warps` * 32; returns
 // its part of the sums.  raise: report bad lengths.
-__device__ __forceinline__ Shapes gather_shapes(const PagedArgs &a, Shape *at, int warp, int warps,
+__device__ __forceinline__ Shapes gather_shapes(const PagedArgs &a, Shape *at, int cap, int warp, int warps,
                                                 int pos, int bn, bool raise) {
   float work = 0.f, pairs = 0.f, long_pairs = 0.f;
   int longest = 0, rows = 0;
@@ -158,14 +159,14 @@ __device__ __forceinline__ Shapes gather_shapes(const PagedArgs &a, Shape *at, i
     const PagedSeq s = paged_seq(a, i);
     if (raise && s.err) raise_error(a.err, s.err);
     const Shape x = shape_of(a, s, pos, bn);
-    if (i < kMaxShapes) at[i] = x;
+    if (i < cap) at[i] = x;
     work += (float)x.tiles * (float)x.steps;
     pairs += (float)x.tiles;
     if (x.tiles > 1) long_pairs += (float)x.tiles;
     longest = max(longest, x.steps);
     rows = max(rows, min(s.lq, pos));
   }
-  return Shapes{at, warp_sum(work), warp_sum(pairs), warp_sum(long_pairs),
+  return Shapes{at, cap, warp_sum(work), warp_sum(pairs), warp_sum(long_pairs),
                 __reduce_max_sync(0xffffffffu, longest), __reduce_max_sync(0xffffffffu, rows)};
 }
 
@@ -242,7 +243,7 @@ __device__ __forceinline__ bool find_item(const PagedArgs &a, const Shapes &sh, 
   const int nh = a.pack > 1 ? a.hkv : a.hq;
   const auto shape = [&](int i) {
     if (i >= a.batch) return Shape{0, 0};
-    return i < kMaxShapes ? sh.at[i] : shape_of(a, paged_seq(a, i), pos, bn);
+    return i < sh.cap ? sh.at[i] : shape_of(a, paged_seq(a, i), pos, bn);
   };
   const Shape first = shape(lane);
   int piece_steps = INT32_MAX;
@@ -384,8 +385,8 @@ struct Shared {
   Shapes sums[kMaxWarps];  // of the warps' sequences
   uint32_t tmem_base;
   int abort;
-  int issued;              // K and V tiles whose copies have been issued (2 j: K of step j)
-  Box box[32];             // boxes of the next steps
+  int k_issued, v_issued;  // steps whose copies have been issued
+  Box box[2][32];          // boxes of this and the next 32 boxes' steps
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -513,10 +514,12 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pg = a.pack;
-  Shapes shapes{reinterpret_cast<Shape *>(smem), 0.f, 0.f, 0.f, 0, 0};
+  // paged_join_kernel may come up as the last blocks of this one run
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  Shapes shapes{reinterpret_cast<Shape *>(smem), kMaxShapes, 0.f, 0.f, 0.f, 0, 0};
   constexpr int kGather = C::kThreads / 32;
   if (warp * 32 < a.batch) {
-    const Shapes sum = gather_shapes(a, shapes.at, warp, kGather, tile_pos, BN, blockIdx.x == 0);
+    const Shapes sum = gather_shapes(a, shapes.at, kMaxShapes, warp, kGather, tile_pos, BN, blockIdx.x == 0);
     if (lane == 0) sh.sums[warp] = sum;
   }
   if (a.batch > 32) __syncthreads();  // (else warp 0 has gathered all)
@@ -557,7 +560,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
     mbar_init(&sh.all_done, 1);
     sh.wait_ns = a.wait_ns;
     sh.abort = 0;
-    sh.issued = 0;
+    sh.k_issued = sh.v_issued = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -578,7 +581,9 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
       // All lanes look pages up; one thread issues the copies, in stretches behind
       // which the lanes meet.
       if (nt > 0) {
-        const int boxes = BN / box_rows, per = 32 / boxes;  // powers of two
+        // boxes of a step and steps of 32 boxes, powers of two (no divisions: one thread's
+        // instructions are what a step can wait for)
+        const int lb = __ffs(BN / box_rows) - 1, boxes = 1 << lb, per = 32 >> lb;  // lb <= 2
         const int key_lo = n_lo * BN;
         Box ahead = early;
         if (elect_one()) {
@@ -587,36 +592,55 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
             tma_load_3d(q_s + c * kBM * 128, &tq, &sh.q_full, c * 64, h, sq.q0 + it.m0);
         }
         __syncwarp();
-        // copies of the steps [j0, j1)
+        const auto copy = [&](int j, uint8_t *dst, const CUtensorMap *map, uint64_t *full,
+                              uint64_t *empty) {
+          const int st = j % ST;
+          const Box *bx = &sh.box[0][j << lb & 63];
+          if (!wait_bar(sh, &empty[st], ((j / ST) & 1) ^ 1, a.err)) return false;
+          uint8_t *to = dst + st * C::kKVBytes;
+          const auto boxes_of = [&](auto count) {
+            constexpr int n = decltype(count)::value, kBytes = C::kKVBytes / n;
+            Box x[n];
+            uint32_t bytes = 0;
+#pragma unroll
+            for (int b = 0; b < n; ++b) {
+              x[b] = bx[b];
+              bytes += x[b].page >= 0 ? kBytes : 0;
+            }
+            mbar_expect_tx(&full[st], bytes);
+#pragma unroll
+            for (int b = 0; b < n; ++b) {
+              if (x[b].page < 0) continue;
+#pragma unroll
+              for (int c = 0; c < C::kCols; ++c)
+                tma_load_4d(to + c * (BN * 128) + b * (BN / n * 128), map, &full[st], c * 64, kvh,
+                            x[b].slot, x[b].page);
+            }
+          };
+          static_assert(BN == 64, "boxes of 64, 32 or 16 keys");
+          if (lb == 0)
+            boxes_of(std::integral_constant<int, 1>{});
+          else if (lb == 1)
+            boxes_of(std::integral_constant<int, 2>{});
+          else
+            boxes_of(std::integral_constant<int, 4>{});
+          return true;
+        };
+        // V of the steps [j0, j1), and K one step ahead: the next scores are
+        // computed before this step's values are needed
         const auto issue = [&](int j0, int j1) {
           if (elect_one()) {
             for (int j = j0; j < j1; ++j) {
-              const int st = j % ST;
-              const uint32_t ph = (j / ST) & 1;
-              const Box *bx = &sh.box[j % per * boxes];
-              int n = 0;
-              for (int b = 0; b < boxes; ++b) n += bx[b].page >= 0;
-              const uint32_t bytes = n * box_rows * D * 2;
-              if (!wait_bar(sh, &sh.k_empty[st], ph ^ 1, a.err)) break;
-              mbar_expect_tx(&sh.k_full[st], bytes);
-              for (int b = 0; b < boxes; ++b) {
-                const Box x = bx[b];
-                if (x.page < 0) continue;
-                for (int c = 0; c < C::kCols; ++c)
-                  tma_load_4d(k_s + st * C::kKVBytes + c * (BN * 128) + b * box_rows * 128, &tk,
-                              &sh.k_full[st], c * 64, kvh, x.slot, x.page);
+              if (j == 0) {
+                copy(0, k_s, &tk, sh.k_full, sh.k_empty);
+                sh.k_issued = 1;
               }
-              sh.issued = 2 * j + 1;
-              if (!wait_bar(sh, &sh.v_empty[st], ph ^ 1, a.err)) break;
-              mbar_expect_tx(&sh.v_full[st], bytes);
-              for (int b = 0; b < boxes; ++b) {
-                const Box x = bx[b];
-                if (x.page < 0) continue;
-                for (int c = 0; c < C::kCols; ++c)
-                  tma_load_4d(v_s + st * C::kKVBytes + c * (BN * 128) + b * box_rows * 128, &tv,
-                              &sh.v_full[st], c * 64, kvh, x.slot, x.page);
+              if (j + 1 < nt) {
+                if (!copy(j + 1, k_s, &tk, sh.k_full, sh.k_empty)) break;
+                sh.k_issued = j + 2;
               }
-              sh.issued = 2 * j + 2;
+              if (!copy(j, v_s, &tv, sh.v_full, sh.v_empty)) break;
+              sh.v_issued = j + 1;
             }
           }
           __syncwarp();
@@ -635,17 +659,17 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
           if (lane == 0) mbar_arrive(bar);
           __syncwarp();
         };
-        for (int j0 = 0; j0 < nt; j0 += per) {
-          if (__any_sync(0xffffffffu, ahead.page == -2)) {
-            if (lane == 0) {
-              raise_error(a.err, kErrPageOutOfRange);
-              *(volatile int *)&sh.abort = 1;
-            }
-            __syncwarp();
-            break;
-          }
-          sh.box[lane] = ahead;
-          ahead = fetch_boxes(a, it, pc, boxes, box_rows, key_lo, (j0 + per) * boxes);
+        bool bad = __any_sync(0xffffffffu, ahead.page == -2);
+        if (!bad) {
+          sh.box[0][lane] = ahead;
+          ahead = fetch_boxes(a, it, pc, boxes, box_rows, key_lo, 32);
+        }
+        for (int j0 = 0; !bad && j0 < nt; j0 += per) {
+          // the boxes of the steps behind these (K is a step ahead)
+          bad = __any_sync(0xffffffffu, ahead.page == -2);
+          if (bad) break;
+          sh.box[(j0 << lb >> 5) + 1 & 1][lane] = ahead;
+          ahead = fetch_boxes(a, it, pc, boxes, box_rows, key_lo, j0 * boxes + 64);
           __syncwarp();
           const int j1 = min(nt, j0 + per);
           int j = j0;
@@ -657,16 +681,21 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
           issue(j, j1);
           if (__any_sync(0xffffffffu, *(volatile int *)&sh.abort)) break;
         }
-        const int issued = *(volatile int *)&sh.issued;
-        if (issued == 2 * nt && back > 0) clean(nt - 1, BN - back, BN, &sh.v_clean[1]);
+        if (bad && lane == 0) {
+          raise_error(a.err, kErrPageOutOfRange);
+          *(volatile int *)&sh.abort = 1;
+        }
+        __syncwarp();
+        const int k_issued = *(volatile int *)&sh.k_issued, v_issued = *(volatile int *)&sh.v_issued;
+        if (v_issued == nt && back > 0) clean(nt - 1, BN - back, BN, &sh.v_clean[1]);
         if (*(volatile int *)&sh.abort) {
           // let the copies in flight land before the block exits
           int *noerr = nullptr;
           mbar_wait(&sh.q_full, 0, noerr);
-          for (int x = max(0, issued - 2 * ST); x < issued; ++x) {
-            const int j = x / 2, st = j % ST;
-            mbar_wait(x % 2 ? &sh.v_full[st] : &sh.k_full[st], (j / ST) & 1, noerr);
-          }
+          for (int j = max(0, k_issued - ST); j < k_issued; ++j)
+            mbar_wait(&sh.k_full[j % ST], (j / ST) & 1, noerr);
+          for (int j = max(0, v_issued - ST); j < v_issued; ++j)
+            mbar_wait(&sh.v_full[j % ST], (j / ST) & 1, noerr);
         }
       }
     } else {
@@ -946,18 +975,18 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
 // pieces joins a share of the pair's rows.
 template <typename T, int D, int BN>
 __global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a, const int tile_pos) {
-  __shared__ Shape at[kMaxShapes];
+  __shared__ Shape at[kJoinShapes];
   __shared__ Shapes sums[4];
   __shared__ Item item;
   __shared__ int written;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp * 32 < a.batch) {
-    const Shapes sum = gather_shapes(a, at, warp, 4, tile_pos, BN, false);
+    const Shapes sum = gather_shapes(a, at, kJoinShapes, warp, 4, tile_pos, BN, false);
     if (lane == 0) sums[warp] = sum;
   }
   __syncthreads();
   if (warp == 0) {
-    Shapes all{at, 0.f, 0.f, 0.f, 0, 0};
+    Shapes all{at, kJoinShapes, 0.f, 0.f, 0.f, 0, 0};
     for (int w = 0; w < 4 && w * 32 < a.batch; ++w) add_shapes(all, sums[w]);
     Item it{};
     it.pieces = 1;
@@ -968,6 +997,9 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a, cons
       written = p.live && it.pieces > 1 ? p.written : 0;
     }
   }
+  // until the main kernel has finished; every block, so that this grid, and with
+  // it the call, does not end before that one
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
   const Item it = item;
   const int n = written, slot0 = it.slot - it.piece * it.stride;
@@ -1023,7 +1055,15 @@ cudaError_t paged(const PagedArgs &a, const PagedPlan &plan, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   count_launches(1);
   if (plan.slots > 0) {
-    paged_join_kernel<T, D, BN><<<(unsigned)plan.items, 128, 0, st>>>(a, plan.tile_pos);
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, paged_join_kernel<T, D, BN>, a, plan.tile_pos);
+    if (e != cudaSuccess) return e;
     count_launches(1);
   }
   return cudaGetLastError();
