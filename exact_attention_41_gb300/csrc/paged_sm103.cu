@@ -385,7 +385,6 @@ struct Shared {
   Shapes sums[kMaxWarps];  // of the warps' sequences
   uint32_t tmem_base;
   int abort;
-  int k_issued, v_issued;  // steps whose copies have been issued
   Box box[2][32];          // boxes of this and the next 32 boxes' steps
 };
 
@@ -560,7 +559,6 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
     mbar_init(&sh.all_done, 1);
     sh.wait_ns = a.wait_ns;
     sh.abort = 0;
-    sh.k_issued = sh.v_issued = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -596,7 +594,6 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
                               uint64_t *empty) {
           const int st = j % ST;
           const Box *bx = &sh.box[0][j << lb & 63];
-          if (!wait_bar(sh, &empty[st], ((j / ST) & 1) ^ 1, a.err)) return false;
           uint8_t *to = dst + st * C::kKVBytes;
           const auto boxes_of = [&](auto count) {
             constexpr int n = decltype(count)::value, kBytes = C::kKVBytes / n;
@@ -618,32 +615,36 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
             }
           };
           static_assert(BN == 64, "boxes of 64, 32 or 16 keys");
-          if (lb == 0)
-            boxes_of(std::integral_constant<int, 1>{});
-          else if (lb == 1)
-            boxes_of(std::integral_constant<int, 2>{});
-          else
-            boxes_of(std::integral_constant<int, 4>{});
-          return true;
+          bool ok = false;
+          if (elect_one()) {
+            ok = wait_bar(sh, &empty[st], ((j / ST) & 1) ^ 1, a.err);
+            if (ok) {
+              if (lb == 0)
+                boxes_of(std::integral_constant<int, 1>{});
+              else if (lb == 1)
+                boxes_of(std::integral_constant<int, 2>{});
+              else
+                boxes_of(std::integral_constant<int, 4>{});
+            }
+          }
+          return (bool)__any_sync(0xffffffffu, ok);
         };
         // V of the steps [j0, j1), and K one step ahead: the next scores are
         // computed before this step's values are needed
+        int k_issued = 0, v_issued = 0;  // steps whose copies have been issued
         const auto issue = [&](int j0, int j1) {
-          if (elect_one()) {
-            for (int j = j0; j < j1; ++j) {
-              if (j == 0) {
-                copy(0, k_s, &tk, sh.k_full, sh.k_empty);
-                sh.k_issued = 1;
-              }
-              if (j + 1 < nt) {
-                if (!copy(j + 1, k_s, &tk, sh.k_full, sh.k_empty)) break;
-                sh.k_issued = j + 2;
-              }
-              if (!copy(j, v_s, &tv, sh.v_full, sh.v_empty)) break;
-              sh.v_issued = j + 1;
+          for (int j = j0; j < j1; ++j) {
+            if (j == 0) {
+              copy(0, k_s, &tk, sh.k_full, sh.k_empty);
+              k_issued = 1;
             }
+            if (j + 1 < nt) {
+              if (!copy(j + 1, k_s, &tk, sh.k_full, sh.k_empty)) break;
+              k_issued = j + 2;
+            }
+            if (!copy(j, v_s, &tv, sh.v_full, sh.v_empty)) break;
+            v_issued = j + 1;
           }
-          __syncwarp();
         };
         // zeroes rows [r0, r1) of V tile j once it has landed
         const auto clean = [&](int j, int r0, int r1, uint64_t *bar) {
@@ -686,7 +687,6 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
           *(volatile int *)&sh.abort = 1;
         }
         __syncwarp();
-        const int k_issued = *(volatile int *)&sh.k_issued, v_issued = *(volatile int *)&sh.v_issued;
         if (v_issued == nt && back > 0) clean(nt - 1, BN - back, BN, &sh.v_clean[1]);
         if (*(volatile int *)&sh.abort) {
           // let the copies in flight land before the block exits
@@ -769,7 +769,20 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
     const int r0 = 32 * (warp & 3), r = r0 + lane;  // TMEM lane = row in the tile
     const int first = it.m0;                        // the tile's first query position
     const int rows = min(max(sq.lq - first, 0), tile_pos) * pg;  // its rows in the sequence
-    {
+    if (r0 >= rows) {
+      // No row of the sequence: P is zeros, so that the product reads no leftovers.
+      const uint32_t zeros[16] = {};
+      for (int j = 0; j < nt; ++j) {
+        if (!wait_warp(sh, &sh.s_full[j & 1], (j >> 1) & 1, a.err)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c)
+          tmem_st16(tmem + ((uint32_t)r0 << 16) + C::kSCol0 + (j & 1) * BN + c * 16, zeros);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&sh.p_full[j & 1]);
+      }
+    } else {
       const int i = first + r / pg;  // query position
       const int hr = h + r % pg;     // and query head
       const uint32_t lane_off = (uint32_t)r0 << 16;
