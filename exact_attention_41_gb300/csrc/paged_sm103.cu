@@ -18,34 +18,38 @@
 // Pieces.  With few tiles the keys are cut, so that the call fills whole waves of
 // blocks: all key steps together, and what starting blocks and joining pieces
 // costs, give the steps of a piece (choose_piece).  Pieces of a cut row write a
-// normalised fp32 O and its log2-sum; the block that writes the last piece of a
-// tile joins them, in piece order, so the result is the same every run.
+// normalised fp32 O and its log2-sum; paged_join_kernel joins them, in piece order,
+// so the result is the same every run.
 //
 // Keys.  A K or V tile of BN keys is one TMA box where a page holds a multiple
-// of BN keys, and otherwise one box per gcd(page_size, BN) keys, issued by as
-// many lanes; a lane holds the page of one of the next 32 boxes and looks up that
-// of the 32 behind them.  Boxes without a visible key are not loaded and their
-// table entries not read.  Slots outside the block's visible keys may hold
-// anything, and 0 * NaN would reach O, so the V producer zeroes those rows of the
+// of BN keys, and otherwise one box per gcd(page_size, BN) keys; a lane of the
+// producer looks up the page of one of the next 32 boxes while those of the 32
+// before are copied.  Boxes without a visible key are not loaded and their table
+// entries not read.  Slots outside the block's visible keys may hold
+// anything, and 0 * NaN would reach O, so the producer zeroes those rows of the
 // first and last V tile in shared memory before their product is issued; in K
 // they only reach scores that the mask overwrites.
 //
-// Roles.  Warp 0 finds the item and loads Q and K, warp 6 loads V, warp 1 issues
-// the products, warps 2-5 are the softmax, one row a thread; those whose 32 rows
-// are all beyond the sequence do nothing.
+// Roles.  Warp 0 finds the item and is the producer, warp 1 issues the products,
+// warps 2-5 are the softmax, one row a thread; those whose 32 rows are all beyond
+// the sequence write zeros to P.  TMA and tensor-core instructions come from one
+// lane at a time, with its warp waiting behind them.  (Copies issued by a lane per
+// box from two warps, softmax warps that left early and a join in the block that
+// came last were up to a quarter faster on small pages and few tokens; replayed
+// some thousand times from a graph, calls ended in an illegal instruction.)
 //
 // What bounds it (measured copy 6.8 TB/s, cuBLAS bf16 1.9 PFLOP/s):
-//   64 single tokens, caches up to 32K, 32/8 heads of 128: 7.1 TB/s; the memory.
-//   24 drafts of 2-9 tokens, 64/8 heads of 64: 4.9 TB/s; blocks' starts and the
-//     joining of pieces, in two waves.
-//   a chunk of 8192 behind 24K, 32/8 heads of 128: 1.46 PFLOP/s; products and
+//   64 single tokens, caches up to 32K, 32/8 heads of 128: 7.0 TB/s; the memory.
+//   24 drafts of 2-9 tokens, 64/8 heads of 64, 16-token pages: 4.0 TB/s; one lane
+//     issues eight copies a step (64-token pages 4.6 TB/s).
+//   a chunk of 8192 behind 24K, 32/8 heads of 128: 1.47 PFLOP/s; products and
 //     softmax of two blocks a SM, as in the dense forward.
-//   47 single tokens and a chunk of 2001: 3.5 TB/s and 0.81 PFLOP/s at once; a
+//   47 single tokens and a chunk of 2001: 3.3 TB/s and 0.76 PFLOP/s at once; a
 //     chunk's block beside a token's has the tensor cores to itself and waits for
 //     its own softmax.
-//   12 chunks of 100-1000 in a window of 1024, 8/4 heads of 256: 0.5 PFLOP/s; one
-//     block a SM, whose start (5 us) and end (4 us) nothing covers.  Long chunks
-//     there run at 1.25 PFLOP/s.
+//   12 chunks of 100-1000 in a window of 1024, 8/4 heads of 256: 0.53 PFLOP/s; one
+//     block a SM, whose start and end nothing covers.  Long chunks there run at
+//     1.2 PFLOP/s.
 #include <algorithm>
 #include <numeric>
 #include <type_traits>
@@ -63,9 +67,9 @@ constexpr int kMaxStages = 5;
 constexpr int kMaxWarps = 6;
 constexpr int kMinPieceSteps = 4;          // shortest piece worth a block and a partial result
 constexpr int kBlockSteps = 8;             // a block's start and end, in steps
-// what joining adds to a call, in steps: a step per so many values of a piece,
-// and once (rows on their way to the workspace and back) per so many of a tile
-constexpr float kJoinRate = 5000.f, kJoinBase = 1400.f;
+// what joining adds to a call, in steps: the second kernel, and one per so many
+// values of a tile (on their way to the workspace and back)
+constexpr float kJoinSteps = 6.f, kJoinRate = 2000.f;
 
 // One 128-row query tile per block and BN keys per step.  TMEM: O in columns
 // [0, D), two S/P buffers behind it, so S of the next step is computed while the
@@ -198,25 +202,20 @@ __device__ __forceinline__ int choose_piece(const PagedArgs &a, float work, floa
     return max(kMinPieceSteps, (int)fminf(__fdividef(work, n) * 1.0001f, 1e9f) + 1);
   };
   // Pieces make waves of blocks, and a wave that is started for a few of them
-  // is lost.  Pairs of a tile and a head end in a part of a piece, half of one on average: n full
-  // pieces make n + pairs / 2.  Take the number of waves whose time -- a piece's
-  // steps, and kBlockSteps for a block's start and end, and the joining of them --
-  // is least.  (24 sequences of 2-9 tokens, d = 64: 2.3 waves 127 us, just below
-  // two 109.)  Of few pairs with many rows the wave need not be full: n pieces of
-  // L steps in all take L / n + join n, least at a piece of sqrt(join L) steps.
-  // (32 tokens, 8 KV heads, behind 4096: 1 piece 45 us, 4 32, 8 36, 16 47.)
+  // is lost.  Pairs of a tile and a head end in a part of a piece, half of one on
+  // average: n full pieces make n + pairs / 2.  Take the number of waves whose time
+  // -- a piece's steps, and kBlockSteps for a block's start and end, and the join
+  // -- is least.  (24 sequences of 2-9 tokens, d = 64: 2 pieces a row 132 us, 3 140,
+  // 8 149, chosen so 117.  32 tokens behind 4096: 1 piece 47 us, 4 30, 8 and more 24.)
   const float values = (float)(rows * a.pack) * (float)a.d;
-  const float join = values * (1.f / kJoinRate);        // per piece
-  const float join0 = 2.f + values * (1.f / kJoinBase); // once
+  const float join0 = kJoinSteps + values * (1.f / kJoinRate);
   int ps = least(2.f * wave);  // more pairs than max_waves hold
   float best = INFINITY, room = 0.f;
   for (int k = 1; k <= a.max_waves; ++k) {
     const float blocks = (float)k * wave;
     if (pairs >= 0.9f * blocks) continue;
     int p = least(0.98f * blocks - 0.5f * pairs);
-    if (k == 1) p = max(p, (int)sqrtf(join * (float)longest));
-    const float time = (float)k * (float)(p + kBlockSteps) + join0 +
-                       join * __fdividef((float)longest, (float)p);
+    const float time = (float)k * (float)(p + kBlockSteps) + join0;
     if (time < best) {
       best = time;
       ps = p;
@@ -234,35 +233,47 @@ __device__ __forceinline__ int choose_piece(const PagedArgs &a, float work, floa
   return ps;
 }
 
+__device__ __forceinline__ Shape shape_at(const PagedArgs &a, const Shapes &sh, int i, int pos,
+                                          int bn) {
+  if (i >= a.batch) return Shape{0, 0};
+  return i < sh.cap ? sh.at[i] : shape_of(a, paged_seq(a, i), pos, bn);
+}
+
+// Steps of a piece where num_splits is 0 (INT32_MAX: nothing is cut).  Whole warp.
+struct Cut {
+  int steps;
+  float inv;
+};
+__device__ __forceinline__ Cut cut_of(const PagedArgs &a, const Shapes &sh, int pos, int bn) {
+  Cut cut{INT32_MAX, 0.f};
+  if (a.num_splits == 0) {
+    const float nh = (float)(a.pack > 1 ? a.hkv : a.hq);
+    cut.steps = choose_piece(a, sh.work * nh, sh.pairs * nh, sh.longest, sh.rows, [&](int ps) {
+      const float inv = __frcp_rn((float)ps);
+      float n = 0.f;
+      for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        const Shape x = shape_at(a, sh, b0 + (threadIdx.x & 31), pos, bn);
+        n += (float)x.tiles * (float)div_up(x.steps, ps, inv);
+      }
+      return warp_sum(n) * nh;
+    });
+    cut.inv = __frcp_rn((float)cut.steps);
+  }
+  return cut;
+}
+
 // Item `idx` of the call; false behind the last one.  Whole warp; `pos` query
 // positions per block.  Counts saturate at INT32_MAX, above every block index, so
 // offsets that overlap (more rows than total_q) only lose work, which is flagged.
-__device__ __forceinline__ bool find_item(const PagedArgs &a, const Shapes &sh, uint32_t idx,
-                                          int pos, int bn, Item &it) {
+__device__ __forceinline__ bool find_item(const PagedArgs &a, const Shapes &sh, const Cut &cut,
+                                          uint32_t idx, int pos, int bn, Item &it) {
   const int lane = threadIdx.x & 31;
   const int nh = a.pack > 1 ? a.hkv : a.hq;
-  const auto shape = [&](int i) {
-    if (i >= a.batch) return Shape{0, 0};
-    return i < sh.cap ? sh.at[i] : shape_of(a, paged_seq(a, i), pos, bn);
-  };
+  const auto shape = [&](int i) { return shape_at(a, sh, i, pos, bn); };
   const Shape first = shape(lane);
-  int piece_steps = INT32_MAX;
-  float inv_steps = 0.f;
-  if (a.num_splits == 0) {
-    piece_steps = choose_piece(a, sh.work * (float)nh, sh.pairs * (float)nh, sh.longest, sh.rows, [&](int ps) {
-      const float inv = __frcp_rn((float)ps);
-      float n = (float)first.tiles * (float)div_up(first.steps, ps, inv);
-      for (int b0 = 32; b0 < a.batch; b0 += 32) {
-        const Shape x = shape(b0 + lane);
-        n += (float)x.tiles * (float)div_up(x.steps, ps, inv);
-      }
-      return warp_sum(n) * (float)nh;
-    });
-    inv_steps = __frcp_rn((float)piece_steps);
-  }
   const auto pieces_of = [&](const Shape &x) {
     if (a.num_splits > 0) return max(1, min(a.num_splits, x.steps));
-    return x.steps <= piece_steps ? 1 : div_up(x.steps, piece_steps, inv_steps);
+    return x.steps <= cut.steps ? 1 : div_up(x.steps, cut.steps, cut.inv);
   };
   const auto times = [&](const Shape &x, int p) {
     return (float)x.tiles * (float)(nh * p) > 2e9f ? (uint32_t)INT32_MAX
@@ -302,12 +313,12 @@ __device__ __forceinline__ bool find_item(const PagedArgs &a, const Shapes &sh, 
       if (lane >= o) incl = add_sat(incl, up);
     }
     const uint32_t hit = __ballot_sync(0xffffffffu, idx < add_sat(base, incl));
-    const uint32_t cut = pieces > 1 ? all : 0;  // slots
+    const uint32_t cut_items = pieces > 1 ? all : 0;  // slots
     if (hit) {
       const int src = __ffs(hit) - 1;
       it.seq = b0 + src;
       it.s = paged_seq(a, it.seq);
-      slots = add_sat(slots, __reduce_add_sync(0xffffffffu, lane < src ? cut : 0));
+      slots = add_sat(slots, __reduce_add_sync(0xffffffffu, lane < src ? cut_items : 0));
       const uint32_t local = idx - base - __shfl_sync(0xffffffffu, incl - n, src);
       it.pieces = __shfl_sync(0xffffffffu, pieces, src);
       const int tiles = __shfl_sync(0xffffffffu, x.tiles, src);
@@ -324,7 +335,7 @@ __device__ __forceinline__ bool find_item(const PagedArgs &a, const Shapes &sh, 
       return it.m0 >= 0;
     }
     base = add_sat(base, __shfl_sync(0xffffffffu, incl, 31));
-    slots = add_sat(slots, __reduce_add_sync(0xffffffffu, cut));
+    slots = add_sat(slots, __reduce_add_sync(0xffffffffu, cut_items));
   }
   return false;
 }
@@ -355,7 +366,7 @@ __device__ __forceinline__ Piece piece_of(const PagedArgs &a, const Item &it, in
 }
 
 // Pages and slots of the piece's key boxes b0 .. b0 + 31, one per lane.  The
-// producers keep 32 in hand and the next 32 on their way: a look-up per step
+// producer has 32 in hand and the next 32 on their way: a look-up per step
 // would add a trip to L2 or further to it.
 struct Box {
   int page, slot;  // page -1: no visible key, -2: outside the pool
@@ -528,7 +539,8 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
     for (int w = 0; w < kGather && w * 32 < a.batch; ++w) add_shapes(shapes, sh.sums[w]);
     Item it{};
     it.pieces = 1;
-    const bool found = find_item(a, shapes, blockIdx.x, tile_pos, BN, it);
+    const bool found =
+        find_item(a, shapes, cut_of(a, shapes, tile_pos, BN), blockIdx.x, tile_pos, BN, it);
     const Piece p = piece_of(a, it, tile_pos, BN, found);
     early = fetch_boxes(a, it, p, BN / box_rows, box_rows, p.n_lo * BN, 0);
     if (lane == 0) {
@@ -984,45 +996,57 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-// Joins the pieces of cut rows.  Blocks are the main kernel's: each of a pair's
-// pieces joins a share of the pair's rows.
+// Joins the pieces of cut rows.  Its blocks run over the main kernel's items; each
+// of a pair's pieces joins a share of the pair's rows.  One wave of blocks: they come
+// up while the main kernel's last ones run, and have their items found by the time
+// those end.
 template <typename T, int D, int BN>
 __global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a, const int tile_pos) {
   __shared__ Shape at[kJoinShapes];
   __shared__ Shapes sums[4];
   __shared__ Item item;
-  __shared__ int written;
+  __shared__ int written;  // pieces of the item's pair; 0 not cut, -1 no item
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp * 32 < a.batch) {
     const Shapes sum = gather_shapes(a, at, kJoinShapes, warp, 4, tile_pos, BN, false);
     if (lane == 0) sums[warp] = sum;
   }
   __syncthreads();
+  Shapes all{at, kJoinShapes, 0.f, 0.f, 0.f, 0, 0};
+  Cut cut{};
   if (warp == 0) {
-    Shapes all{at, kJoinShapes, 0.f, 0.f, 0.f, 0, 0};
     for (int w = 0; w < 4 && w * 32 < a.batch; ++w) add_shapes(all, sums[w]);
-    Item it{};
-    it.pieces = 1;
-    const bool found = find_item(a, all, blockIdx.x, tile_pos, BN, it);
-    const Piece p = piece_of(a, it, tile_pos, BN, found);
-    if (lane == 0) {
-      item = it;
-      written = p.live && it.pieces > 1 ? p.written : 0;
-    }
+    cut = cut_of(a, all, tile_pos, BN);
   }
-  // until the main kernel has finished; every block, so that this grid, and with
-  // it the call, does not end before that one
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  __syncthreads();
-  const Item it = item;
-  const int n = written, slot0 = it.slot - it.piece * it.stride;
-  if (n == 0 || slot0 + (n - 1) * it.stride >= a.slots) return;
-  const int rows = min(it.s.lq - it.m0, tile_pos) * a.pack;
-  const int lo = rows * it.piece / n, hi = rows * (it.piece + 1) / n;
-  if (hi - lo <= 4)
-    join_rows<T, D, 4, 1, 4>(a, it, n, slot0, lo, hi, warp);
-  else
-    join_rows<T, D, 4, 2, 4>(a, it, n, slot0, lo, hi, warp);
+  for (uint32_t idx = blockIdx.x;; idx += gridDim.x) {
+    if (warp == 0) {
+      Item it{};
+      it.pieces = 1;
+      const bool any = a.num_splits > 1 || cut.steps < INT32_MAX;
+      const bool found = any && find_item(a, all, cut, idx, tile_pos, BN, it);
+      const Piece p = piece_of(a, it, tile_pos, BN, found);
+      if (lane == 0) {
+        item = it;
+        written = !found ? -1 : p.live && it.pieces > 1 ? p.written : 0;
+      }
+    }
+    // until the main kernel has finished; every block, so that this grid, and with
+    // it the call, does not end before that one
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __syncthreads();
+    const Item it = item;
+    const int n = written, slot0 = it.slot - it.piece * it.stride;
+    if (n < 0) return;
+    if (n > 0 && slot0 + (n - 1) * it.stride < a.slots) {
+      const int rows = min(it.s.lq - it.m0, tile_pos) * a.pack;
+      const int lo = rows * it.piece / n, hi = rows * (it.piece + 1) / n;
+      if (hi - lo <= 4)
+        join_rows<T, D, 4, 1, 4>(a, it, n, slot0, lo, hi, warp);
+      else
+        join_rows<T, D, 4, 2, 4>(a, it, n, slot0, lo, hi, warp);
+    }
+    __syncthreads();
+  }
 }
 
 // (page, slot, head, D) pool, box {64, 1, box_rows, 1}, 128-byte swizzle.
@@ -1071,6 +1095,8 @@ cudaError_t paged(const PagedArgs &a, const PagedPlan &plan, cudaStream_t st) {
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
+    // (a wave: by registers 6 blocks a SM, at d = 256 4)
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(plan.items, a.wave / C::kCtas * (D <= 128 ? 6 : 4)));
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
     cfg.attrs = &at;
@@ -1103,8 +1129,14 @@ PagedPlan paged_plan(int batch, int total_q, int hq, int hkv, int d, int num_spl
   // sum of ceil(n_i / pos) over sequences of sum total_q
   p.tiles = ((int64_t)total_q / p.tile_pos + std::min(batch, total_q)) * nh;
   p.num_splits = std::min(num_splits, kMaxSplits);
-  // enough tiles for several waves even if no sequence leaves one half empty
-  if (num_splits == 0 && ((int64_t)total_q + p.tile_pos - 1) / p.tile_pos * nh >= 4 * wave)
+  // Not cut, so that there is no second kernel and hardly a block without work:
+  // chunks that fill several waves of tiles whatever the lengths (where no cache is
+  // long: one and a half; 12 chunks of 100-1000 in a window, 2.2 waves, 86 us with
+  // the choice left to the device, 78 so), and caches so short that joining costs
+  // what cutting saves (3 chunks of 64 behind 1000 tokens 21.8 and 19.0 us; 8
+  // single tokens behind up to 2048 20.3 and 24.2).
+  const int64_t full = ((int64_t)total_q + p.tile_pos - 1) / p.tile_pos * nh;
+  if (num_splits == 0 && (full >= 4 * wave || (2 * full >= 3 * wave && keys <= 16384) || keys <= 1280))
     p.num_splits = 1;
   p.wave = (int)wave;
   if (p.num_splits == 0) {
