@@ -155,8 +155,8 @@ struct Shapes {
 };
 // One warp's share, sequences `warp` * 32 + lane and on by `warps` * 32; returns
 // its part of the sums.  raise: report bad lengths.
-__device__ __forceinline__ Shapes gather_shapes(const PagedArgs &a, Shape *at, int cap, int warp, int warps,
-                                                int pos, int bn, bool raise) {
+__device__ __forceinline__ Shapes gather_shapes(const PagedArgs &a, Shape *at, int cap, int warp,
+                                                int warps, int pos, int bn, bool raise) {
   float work = 0.f, pairs = 0.f, long_pairs = 0.f;
   int longest = 0, rows = 0;
   for (int i = warp * 32 + (threadIdx.x & 31); i < a.batch; i += warps * 32) {
@@ -529,7 +529,8 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
   Shapes shapes{reinterpret_cast<Shape *>(smem), kMaxShapes, 0.f, 0.f, 0.f, 0, 0};
   constexpr int kGather = C::kThreads / 32;
   if (warp * 32 < a.batch) {
-    const Shapes sum = gather_shapes(a, shapes.at, kMaxShapes, warp, kGather, tile_pos, BN, blockIdx.x == 0);
+    const Shapes sum = gather_shapes(a, shapes.at, kMaxShapes, warp, kGather, tile_pos, BN,
+                                     blockIdx.x == 0);
     if (lane == 0) sh.sums[warp] = sum;
   }
   if (a.batch > 32) __syncthreads();  // (else warp 0 has gathered all)
@@ -588,8 +589,8 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
   if (warp < C::kSoftmaxWarp0) {
     if (warp == 0) {
       // ---------------------------------------------------------- producer
-      // All lanes look pages up; one thread issues the copies, in stretches behind
-      // which the lanes meet.
+      // All lanes look pages up; one issues the copies of a tile, for which the
+      // others wait.
       if (nt > 0) {
         // boxes of a step and steps of 32 boxes, powers of two (no divisions: one thread's
         // instructions are what a step can wait for)
