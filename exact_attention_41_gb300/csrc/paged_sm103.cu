@@ -40,8 +40,8 @@
 //
 // What bounds it (measured copy 6.8 TB/s, cuBLAS bf16 1.9 PFLOP/s):
 //   64 single tokens, caches up to 32K, 32/8 heads of 128: 7.0 TB/s; the memory.
-//   24 drafts of 2-9 tokens, 64/8 heads of 64, 16-token pages: 4.0 TB/s; one lane
-//     issues eight copies a step (64-token pages 4.6 TB/s).
+//   24 drafts of 2-9 tokens, 64/8 heads of 64, 16-token pages: 4.2 TB/s; one lane
+//     issues eight copies a step (64-token pages 4.7 TB/s).
 //   a chunk of 8192 behind 24K, 32/8 heads of 128: 1.47 PFLOP/s; products and
 //     softmax of two blocks a SM, as in the dense forward.
 //   47 single tokens and a chunk of 2001: 3.3 TB/s and 0.76 PFLOP/s at once; a
@@ -206,7 +206,7 @@ __device__ __forceinline__ int choose_piece(const PagedArgs &a, float work, floa
   // average: n full pieces make n + pairs / 2.  Take the number of waves whose time
   // -- a piece's steps, and kBlockSteps for a block's start and end, and the join
   // -- is least.  (24 sequences of 2-9 tokens, d = 64: 2 pieces a row 132 us, 3 140,
-  // 8 149, chosen so 117.  32 tokens behind 4096: 1 piece 47 us, 4 30, 8 and more 24.)
+  // 8 149, chosen so 112.  32 tokens behind 4096: 1 piece 47 us, 4 30, 8 and more 24.)
   const float values = (float)(rows * a.pack) * (float)a.d;
   const float join0 = kJoinSteps + values * (1.f / kJoinRate);
   int ps = least(2.f * wave);  // more pairs than max_waves hold
@@ -628,34 +628,32 @@ __global__ void __launch_bounds__(PagedCfg<D, BN>::kThreads, PagedCfg<D, BN>::kC
             }
           };
           static_assert(BN == 64, "boxes of 64, 32 or 16 keys");
-          bool ok = false;
-          if (elect_one()) {
-            ok = wait_bar(sh, &empty[st], ((j / ST) & 1) ^ 1, a.err);
-            if (ok) {
-              if (lb == 0)
-                boxes_of(std::integral_constant<int, 1>{});
-              else if (lb == 1)
-                boxes_of(std::integral_constant<int, 2>{});
-              else
-                boxes_of(std::integral_constant<int, 4>{});
-            }
+          const bool ok = wait_bar(sh, &empty[st], ((j / ST) & 1) ^ 1, a.err);
+          if (ok) {
+            if (lb == 0)
+              boxes_of(std::integral_constant<int, 1>{});
+            else if (lb == 1)
+              boxes_of(std::integral_constant<int, 2>{});
+            else
+              boxes_of(std::integral_constant<int, 4>{});
           }
-          return (bool)__any_sync(0xffffffffu, ok);
+          return ok;
         };
         // V of the steps [j0, j1), and K one step ahead: the next scores are
         // computed before this step's values are needed
         int k_issued = 0, v_issued = 0;  // steps whose copies have been issued
         const auto issue = [&](int j0, int j1) {
           for (int j = j0; j < j1; ++j) {
-            if (j == 0) {
-              copy(0, k_s, &tk, sh.k_full, sh.k_empty);
-              k_issued = 1;
+            int done = 0;
+            if (elect_one()) {
+              if (j == 0) copy(0, k_s, &tk, sh.k_full, sh.k_empty);
+              done = j + 1 >= nt || copy(j + 1, k_s, &tk, sh.k_full, sh.k_empty);
+              if (done && copy(j, v_s, &tv, sh.v_full, sh.v_empty)) done = 2;
             }
-            if (j + 1 < nt) {
-              if (!copy(j + 1, k_s, &tk, sh.k_full, sh.k_empty)) break;
-              k_issued = j + 2;
-            }
-            if (!copy(j, v_s, &tv, sh.v_full, sh.v_empty)) break;
+            const unsigned k_ok = __ballot_sync(0xffffffffu, done >= 1);
+            const unsigned v_ok = __ballot_sync(0xffffffffu, done == 2);
+            k_issued = k_ok ? min(j + 2, nt) : max(k_issued, 1);
+            if (!v_ok) break;
             v_issued = j + 1;
           }
         };
